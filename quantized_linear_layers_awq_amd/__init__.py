@@ -1,6 +1,8 @@
-"""Fused W4A16 / W8A16 linear layer for AMD MI355X (gfx950).
+"""Fused W4A16 / W8A16 linear layer for AMD MI355X (gfx950), and the attention
+over a paged key-value cache that stands between a decoder layer's linears.
 
-Thin binding over ``libtilefuse.so`` (C ABI declared in ``include/tilefuse.h``).
+Thin binding over ``libtilefuse.so`` (C ABI declared in ``include/tilefuse.h``
+and ``include/tilefuse_attention.h``).
 Each ``tf_*`` function here has the name of the C entry point it calls and
 only marshals arguments: torch supplies device memory and the current
 stream, every step of the computation runs in the HIP kernels.  There is no
@@ -57,6 +59,19 @@ from ._binding import (  # noqa: F401
     tf_status_string,
     tf_workspace_bytes,
     tf_workspace_bytes_planned,
+)
+from ._attention import (  # noqa: F401
+    TF_TYPE_BF16,
+    TF_TYPE_F16,
+    tf_attn_decode,
+    tf_attn_decode_workspace_bytes,
+    tf_attn_prefill,
+    tf_attn_prefill_paged,
+    tf_kv_append,
+    tf_kv_compact,
+    tf_kv_compact_workspace_bytes,
+    tf_kv_fork,
+    tf_kv_fork_workspace_bytes,
 )
 
 __all__ = [n for n in dir() if n.startswith(("tf_", "TF_"))] + ["TileFuseError", "load_library"]

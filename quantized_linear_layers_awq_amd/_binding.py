@@ -86,6 +86,23 @@ def load_library():
         L.tf_probe_mfma.restype = I
         L.tf_probe_block_read.argtypes = [I, P, SZ, I64, I64, I64, I, I, P, P]
         L.tf_probe_block_read.restype = I
+        F = ctypes.c_float
+        L.tf_kv_append.argtypes = [I, P, I64, P, I64, P, P, I64, P, I64, I64, P, P, P, I64, I64, I64, I64, I64, P]
+        L.tf_attn_decode_workspace_bytes.argtypes = [I64] * 5
+        L.tf_attn_decode.argtypes = [I, P, I64, I64, P, P, I64, I64, P, I64, P, P, I64, I64, I64, I64, I64, F, P, SZ, P]
+        L.tf_attn_prefill.argtypes = [I, P, I64, I64, P, I64, I64, P, I64, I64, P, P, P, I64, I64, I64, I64, I64, I64,
+                                      I64, F, P]
+        L.tf_attn_prefill_paged.argtypes = [I, P, I64, I64, P, P, I64, I64, P, I64, P, P, P, I64, I64, I64, I64, I64, I64,
+                                            F, P]
+        L.tf_kv_fork_workspace_bytes.argtypes = [I64]
+        L.tf_kv_fork.argtypes = [P, I64, I64, I64, I64, I64, P, P, P, I64, I64, P, P, I64, P, P, P, P, P, SZ, P]
+        L.tf_kv_compact_workspace_bytes.argtypes = [I64]
+        L.tf_kv_compact.argtypes = [P, I64, I64, I64, I64, I64, P, P, I64, I64, P, P, P, P, SZ, P]
+        for n in ("tf_kv_append", "tf_attn_decode", "tf_attn_prefill", "tf_attn_prefill_paged", "tf_kv_fork",
+                  "tf_kv_compact"):
+            getattr(L, n).restype = I
+        for n in ("tf_attn_decode_workspace_bytes", "tf_kv_fork_workspace_bytes", "tf_kv_compact_workspace_bytes"):
+            getattr(L, n).restype = SZ
         _lib = L
         return _lib
 

@@ -144,7 +144,7 @@ template <int D, bool F16, int NT> __global__ __launch_bounds__(64 * kWaves, 2) 
             }
             float top = fmaxf(fmaxf(fmaxf(x[0][0], x[0][1]), fmaxf(x[0][2], x[0][3])),
                               fmaxf(fmaxf(x[1][0], x[1][1]), fmaxf(x[1][2], x[1][3])));
-            top = max_swap32(max_swap16(top)) * a.scale_log2;
+            top = max_swap32(max_swap16(top)) * a.scale_log2 - kHeadroom<F16>;
             if (__builtin_amdgcn_ballot_w64(top > m[nt] + kRescaleSlack)) {
                 const float to = fmaxf(m[nt], top), f = exp2_fast(m[nt] - to);
                 m[nt] = to;

@@ -63,7 +63,8 @@ template <int D, bool F16, bool PAGED> __global__ __launch_bounds__(64 * kWaves,
     const int tile = gridDim.y - 1 - blockIdx.y;
 
     const int q0 = clampi(a.cu_q[seq], 0, a.tokens);
-    const int fresh = clampi(a.cu_q[seq + 1] - q0, 0, min(a.longest, a.tokens - q0));
+    const int all_new = max(clampi(a.cu_q[seq + 1], 0, a.tokens) - q0, 0);
+    const int fresh = min(all_new, a.longest); // tokens past the bound are not computed
     const int64_t row0 = (int64_t)tile * kRowsBlock;
     const int64_t rows = (int64_t)fresh * a.G;
     if (row0 >= rows)
@@ -73,12 +74,12 @@ template <int D, bool F16, bool PAGED> __global__ __launch_bounds__(64 * kWaves,
         keys = clampi(a.lens[seq], 0, a.cache.width << a.cache.page_shift);
     } else {
         k0 = clampi(a.cu_k[seq], 0, a.keys);
-        keys = clampi(a.cu_k[seq + 1] - k0, 0, a.keys - k0);
+        keys = max(clampi(a.cu_k[seq + 1], 0, a.keys) - k0, 0);
     }
     // keys visible to the first and the last token of the workgroup
     const int first = (int)(row0 / a.G);
     const int last = (int)((min(rows, row0 + kRowsBlock) - 1) / a.G);
-    const int shift = keys - fresh + 1;
+    const int shift = keys - all_new + 1;
     const int seen_first = clampi(shift + first, 0, keys), seen_last = clampi(shift + last, 0, keys);
     const int tiles = (seen_last + kKeys - 1) / kKeys;
 
@@ -170,7 +171,7 @@ template <int D, bool F16, bool PAGED> __global__ __launch_bounds__(64 * kWaves,
 #pragma unroll
         for (int i = 1; i < 32; ++i)
             top = fmaxf(top, x[i >> 4][i & 15]);
-        top = max_swap32(top) * a.scale_log2;
+        top = max_swap32(top) * a.scale_log2 - kHeadroom<F16>;
         if (__builtin_amdgcn_ballot_w64(top > m + kRescaleSlack)) {
             const float to = fmaxf(m, top), f = exp2_fast(m - to);
             m = to;
@@ -253,10 +254,9 @@ template <int D, bool F16, bool PAGED> __global__ __launch_bounds__(64 * kWaves,
                     w |= nonfinite_halves<F16>(v[0]) | nonfinite_halves<F16>(v[1]) | nonfinite_halves<F16>(v[2]) |
                          nonfinite_halves<F16>(v[3]);
                 }
+                const bool any = __builtin_amdgcn_ballot_w64(w != 0) != 0;
                 if (lane == 0)
-                    s_bad[wave] = 0;
-                if (w)
-                    s_bad[wave] = 1;
+                    s_bad[wave] = any;
                 wait_lgkmcnt0();
             }
             lds_barrier(); // everybody's copies are there, and tile t - 1 is used up

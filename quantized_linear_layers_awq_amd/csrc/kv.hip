@@ -67,8 +67,10 @@ template <bool F16> __global__ __launch_bounds__(256) void kv_append_kernel(Appe
         if (head < a.hq + a.hkv) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const float x0 = half_lo<F16>(lo[i]), x1 = half_hi<F16>(lo[i]);
-                const float y0 = half_lo<F16>(hi[i]), y1 = half_hi<F16>(hi[i]);
+                // without a rotation the head is zero, whatever it held
+                const uint32_t xs = turns ? lo[i] : 0u, ys = turns ? hi[i] : 0u;
+                const float x0 = half_lo<F16>(xs), x1 = half_hi<F16>(xs);
+                const float y0 = half_lo<F16>(ys), y1 = half_hi<F16>(ys);
                 const float c0 = cs[2 * i], c1 = cs[2 * i + 1], s0 = sn[2 * i], s1 = sn[2 * i + 1];
                 lo[i] = pack_half_x2<F16>(x0 * c0 - y0 * s0, x1 * c1 - y1 * s1);
                 hi[i] = pack_half_x2<F16>(y0 * c0 + x0 * s0, y1 * c1 + x1 * s1);

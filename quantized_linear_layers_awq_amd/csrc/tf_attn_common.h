@@ -16,14 +16,19 @@
 namespace tf {
 
 // Softmax runs in base 2: p = exp2(s c - m) with c = scale log2(e).  The
-// running maximum m starts at kLowest rather than -inf, so that a row with
-// no visible key keeps m finite: every exp2(-inf - m) is 0, the sum stays 0
-// and the row's output is 0.
-constexpr float kLowest = -3.0e38f;
+// running maximum m starts at kLowest, the lowest finite number, rather than
+// at -inf, so that a row with no visible key keeps m finite: every
+// exp2(-inf - m) is 0, the sum stays 0 and the row's output is 0; no finite
+// score lies below it.
+constexpr float kLowest = -3.402823466e38f;
 // O and the sum are rescaled only when a row's maximum has grown by more
 // than this many powers of two: until then p <= 2^8, which bf16, fp16 and
 // the fp32 sums all hold with the same relative precision.
 constexpr float kRescaleSlack = 8.0f;
+// m is held this many powers of two below the maximum: fp16's smallest
+// numbers are 2^-24, and a long row's many small weights must not round to
+// zero there.  p reaches 2^15 at most, inside fp16; bf16 has fp32's range.
+template <bool F16> constexpr float kHeadroom = F16 ? 7.0f : 0.0f;
 
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
 

@@ -332,3 +332,55 @@ def test_other_streams_and_graphs():
         torch.cuda.synchronize()
         assert torch.equal(out, q_.tf_attn_decode(q, kp, vp, tables, n, 3000)), f"replay {it} differs"
         torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_prefill_bound_below_the_new_tokens(d):
+    """Rows up to the bound see the keys they see without it; the rest is not
+    written.  Offsets of the lowest and highest value are clamped."""
+    _, q_ = gpu_or_skip()
+    hq, hkv = 6, 2
+    g = _gen(21)
+    qkv = _normal(g, (90, hq + 2 * hkv, d), torch.bfloat16)
+    q, k, v = qkv[:, :hq], qkv[:, hq:hq + hkv], qkv[:, hq + hkv:]
+    cu = torch.tensor([0, 70, 90], dtype=torch.int32, device=DEV)
+    print("prefill bound", d, flush=True)
+    want = q_.tf_attn_prefill(q, k, v, cu, cu, 70)
+    given = torch.full((90, hq, d), 7.0, dtype=torch.bfloat16, device=DEV)
+    q_.tf_attn_prefill(q, k, v, cu, cu, 33, out=given)
+    torch.cuda.synchronize()
+    assert torch.equal(given[:33], want[:33]) and bool((given[33:70] == 7.0).all())
+    assert torch.equal(given[70:], want[70:])
+    low, high = -(2**31), 2**31 - 1
+    odd = torch.tensor([low, 40, low, high, low], dtype=torch.int32, device=DEV)  # 0..40, none, 0..90, none
+    given = torch.full((90, hq, d), 7.0, dtype=torch.bfloat16, device=DEV)
+    q_.tf_attn_prefill(q, k, v, odd[:3].contiguous(), odd[:3].contiguous(), 90, out=given)
+    torch.cuda.synchronize()
+    assert bool((given[40:] == 7.0).all())
+    _check_prefill(q, lambda s, h: (k[:40, h].double(), v[:40, h].double()), [0, 40], [40], hkv, d ** -0.5, given)
+    given = q_.tf_attn_prefill(q, k, v, odd[2:].contiguous(), odd[2:].contiguous(), 90)
+    torch.cuda.synchronize()
+    _check_prefill(q, lambda s, h: (k[:, h].double(), v[:, h].double()), [0, 90], [90], hkv, d ** -0.5, given)
+
+
+def test_fp16_keeps_the_small_weights_of_a_long_row():
+    """One key of weight 1 and 40000 of weight about 2^-23, each too small for
+    fp16 beside it but a part of 200 together."""
+    _, q_ = gpu_or_skip()
+    n, d, page = 40001, 64, 64
+    pages = -(-n // page)
+    kp = torch.zeros((pages, 1, page, d), dtype=torch.float16, device=DEV)
+    vp = torch.ones_like(kp)
+    q = torch.zeros((1, 1, d), dtype=torch.float16, device=DEV)
+    q[..., 0], kp[0, 0, 0, 0], vp[0, 0, 0] = 1.0, 16.0, 0.0
+    tables = torch.arange(pages, dtype=torch.int32, device=DEV).view(1, -1)
+    lens = torch.tensor([n], dtype=torch.int32, device=DEV)
+    print("small weights", flush=True)
+    for out in (q_.tf_attn_decode(q, kp, vp, tables, lens, n, 1.0),
+                q_.tf_attn_prefill_paged(q, kp, vp, tables, torch.tensor([0, 1], dtype=torch.int32, device=DEV), lens, 1, 1.0)):
+        torch.cuda.synchronize()
+        w = (n - 1) * torch.exp(torch.tensor(-16.0, dtype=torch.float64))
+        want = float(w / (1 + w))
+        # a weight is rounded to half of fp16's smallest step, 2^-25, against a maximum held at 2^7; the sum, one rounding
+        tol = n * 2.0**-32 + 3 * 2.0**-11 * want
+        assert bool(((out.double() - want).abs() <= tol).all()), (out.flatten()[:2].tolist(), want)

@@ -259,3 +259,17 @@ def test_pool_calls_under_a_graph():
         reset()
         step()
         torch.cuda.synchronize()
+
+
+def test_append_without_a_rotation_is_zero_whatever_the_heads_hold():
+    _, q_ = gpu_or_skip()
+    hq, hkv, d, page = 2, 1, 32, 16
+    qkv = torch.full((3, (hq + 2 * hkv) * d), float("inf"), dtype=torch.bfloat16, device=DEV)
+    qkv[1], qkv[2] = float("nan"), 1.0
+    kp, vp = (torch.ones((2, hkv, page, d), dtype=torch.bfloat16, device=DEV) for _ in "kv")
+    print("append without rotation", flush=True)
+    q = q_.tf_kv_append(qkv, _rope(4, d), _ints([0, 0, 0]), _ints([4, 17, 3]), _ints([[0, 1]]), kp, vp, hq)
+    torch.cuda.synchronize()
+    assert bool((q[:2] == 0).all()) and bool((q[2] != 0).all())
+    assert bool((kp[0, 0, 4] == 0).all()) and bool((kp[1, 0, 1] == 0).all())
+    assert bool((vp[0, 0, 4] == float("inf")).all()) and bool(vp[1, 0, 1].isnan().all())

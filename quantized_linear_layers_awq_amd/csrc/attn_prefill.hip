@@ -32,8 +32,6 @@ namespace tf {
 namespace {
 
 constexpr int kWaves = 4;
-constexpr int kRowsWave = 32;
-constexpr int kRowsBlock = kWaves * kRowsWave;
 constexpr int kKeys = 64;
 
 template <int D> __device__ constexpr int k_swz(int row) { return D == 128 ? row & 15 : (row >> 1) & 7; }
@@ -45,7 +43,16 @@ template <bool F16> __device__ __forceinline__ uint32_t nonfinite_halves(uint32_
     return F16 ? ((w & 0x7C007C00u) + 0x04000400u) & 0x80008000u : ((w & 0x7F807F80u) + 0x00800080u) & 0x80008000u;
 }
 
-template <int D, bool F16, bool PAGED> __global__ __launch_bounds__(64 * kWaves, 2) void attn_prefill_kernel(PrefillArgs a)
+// acc + the sum of two packed probabilities, in fp32
+template <bool F16> __device__ __forceinline__ float dot_ones(uint32_t w, float acc)
+{
+    if constexpr (F16)
+        return __builtin_amdgcn_fdot2(__builtin_bit_cast(f16x2, w), f16x2{(_Float16)1.f, (_Float16)1.f}, acc, false);
+    else
+        return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(s16x2, w), s16x2{0x3F80, 0x3F80}, acc, false);
+}
+
+template <int D, bool F16, bool PAGED, int RT> __global__ __launch_bounds__(64 * kWaves, RT == 2 ? 1 : 2) void attn_prefill_kernel(PrefillArgs a)
 {
     constexpr int kSteps = D / 16;          // MFMA steps over channels
     constexpr int kTiles = D / 32;          // 32-channel tiles of O^T
@@ -54,18 +61,19 @@ template <int D, bool F16, bool PAGED> __global__ __launch_bounds__(64 * kWaves,
     constexpr int kRowsPerDma = 1024 / kRow;
     constexpr int kDmas = 16 / kRowsPerDma; // of a wave's 16 rows
     constexpr int kBuf = kKeys * kRow;
-    __shared__ __attribute__((aligned(16))) uint8_t lds[4 * kBuf]; // K, V, K, V
-    __shared__ uint32_t s_bad[kWaves];
+    constexpr int kRowsBlock = kWaves * 32 * RT;
+    extern __shared__ __attribute__((aligned(16))) uint8_t lds[]; // K, K, V, V
+    __shared__ uint32_t s_bad[2][kWaves];
 
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int half = lane >> 5, n = lane & 31;
     const int h = blockIdx.x % a.hkv, seq = blockIdx.x / a.hkv;
-    const int tile = gridDim.y - 1 - blockIdx.y;
+    const int block = gridDim.y - 1 - blockIdx.y;
 
     const int q0 = clampi(a.cu_q[seq], 0, a.tokens);
     const int all_new = max(clampi(a.cu_q[seq + 1], 0, a.tokens) - q0, 0);
     const int fresh = min(all_new, a.longest); // tokens past the bound are not computed
-    const int64_t row0 = (int64_t)tile * kRowsBlock;
+    const int64_t row0 = (int64_t)block * kRowsBlock;
     const int64_t rows = (int64_t)fresh * a.G;
     if (row0 >= rows)
         return;
@@ -77,26 +85,30 @@ template <int D, bool F16, bool PAGED> __global__ __launch_bounds__(64 * kWaves,
         keys = max(clampi(a.cu_k[seq + 1], 0, a.keys) - k0, 0);
     }
     // keys visible to the first and the last token of the workgroup
-    const int first = (int)(row0 / a.G);
-    const int last = (int)((min(rows, row0 + kRowsBlock) - 1) / a.G);
     const int shift = keys - all_new + 1;
-    const int seen_first = clampi(shift + first, 0, keys), seen_last = clampi(shift + last, 0, keys);
+    const int seen_first = clampi(shift + (int)(row0 / a.G), 0, keys);
+    const int seen_last = clampi(shift + (int)((min(rows, row0 + kRowsBlock) - 1) / a.G), 0, keys);
     const int tiles = (seen_last + kKeys - 1) / kKeys;
+    const int whole = seen_first / kKeys; // tiles that every row sees whole
 
-    // this lane's row: token and head
-    const int64_t row = row0 + kRowsWave * wave + n;
-    const int64_t row_in = min(row, rows - 1);
-    const int token = (int)(row_in / a.G), head = h * a.G + (int)(row_in % a.G);
-    const int seen = clampi(shift + token, 0, keys);
-    u32x4 q[kSteps];
-    {
+    // this lane's rows: token, head and visible keys
+    int64_t row[RT], at_out[RT];
+    int seen[RT];
+    u32x4 q[RT][kSteps];
+#pragma unroll
+    for (int r = 0; r < RT; ++r) {
+        row[r] = row0 + 32 * (RT * wave + r) + n;
+        const int64_t in = min(row[r], rows - 1);
+        const int token = (int)(in / a.G), head = h * a.G + (int)(in % a.G);
+        seen[r] = clampi(shift + token, 0, keys);
+        at_out[r] = ((int64_t)(q0 + token) * a.hkv * a.G + head) * D + 4 * half;
         const uint16_t *p = a.q + (int64_t)(q0 + token) * a.q_token + (int64_t)head * a.q_head + 8 * half;
 #pragma unroll
         for (int s = 0; s < kSteps; ++s)
-            q[s] = load16(p + 16 * s);
+            q[r][s] = load16(p + 16 * s);
     }
 
-    // LDS-DMA of tile t into buffer b: unit u of row r lands at u ^ swz(r)
+    // LDS-DMA of tile t: unit u of row i lands at u ^ swz(i)
     const int32_t *const table = PAGED ? a.cache.tables + (int64_t)seq * a.cache.width : nullptr;
     const int d_row = lane / kChunks, d_unit = lane % kChunks;
     const int kstride = PAGED ? kRow : 2 * (int)a.k_token, vstride = PAGED ? kRow : 2 * (int)a.v_token;
@@ -111,28 +123,24 @@ template <int D, bool F16, bool PAGED> __global__ __launch_bounds__(64 * kWaves,
         const int key = kKeys * t + 16 * wave;
         return PAGED && key < keys ? table[key >> a.cache.page_shift] : -1;
     };
-    auto fetch = [&](int t, int b, int page) {
+    auto fetch = [&](bool is_k, int t, int page) {
         const int key = kKeys * t + 16 * wave;
         const int have = clampi(keys - key, 0, 16);
-        Rsrc kr, vr;
+        const uint16_t *base = PAGED ? (is_k ? a.cache.k : a.cache.v) : is_k ? a.k : a.v;
+        Rsrc rs;
         if constexpr (PAGED) {
             const bool ok = page >= 0 && page < a.cache.pages;
             const int64_t at = (((int64_t)(ok ? page : 0) * a.hkv + h) << a.cache.page_shift) + (key & ((1 << a.cache.page_shift) - 1));
-            const uint32_t bytes = ok ? have * kRow : 0;
-            kr = make_rsrc_n(a.cache.k + at * D, bytes);
-            vr = make_rsrc_n(a.cache.v + at * D, bytes);
+            rs = make_rsrc_n(base + at * D, ok ? have * kRow : 0);
         } else {
             const int64_t at = k0 + min(key, max(keys - 1, 0));
-            kr = make_rsrc_n(a.k + at * a.k_token + (int64_t)h * a.k_head, have ? (have - 1) * kstride + kRow : 0);
-            vr = make_rsrc_n(a.v + at * a.v_token + (int64_t)h * a.v_head, have ? (have - 1) * vstride + kRow : 0);
+            rs = make_rsrc_n(base + at * (is_k ? a.k_token : a.v_token) + (int64_t)h * (is_k ? a.k_head : a.v_head),
+                             have ? (have - 1) * (is_k ? kstride : vstride) + kRow : 0);
         }
-        uint8_t *const kb = lds + 2 * b * kBuf + 16 * wave * kRow, *const vb = kb + kBuf;
+        uint8_t *const to = lds + ((is_k ? 0 : 2) + (t & 1)) * kBuf + 16 * wave * kRow;
 #pragma unroll
         for (int i = 0; i < kDmas; ++i)
-            dma16(kr, k_voff[i], 0, kb + 1024 * i);
-#pragma unroll
-        for (int i = 0; i < kDmas; ++i)
-            dma16(vr, v_voff[i], 0, vb + 1024 * i);
+            dma16(rs, is_k ? k_voff[i] : v_voff[i], 0, to + 1024 * i);
     };
 
     // LDS offsets of the operand reads
@@ -144,158 +152,233 @@ template <int D, bool F16, bool PAGED> __global__ __launch_bounds__(64 * kWaves,
     for (int c = 0; c < kTiles; ++c) {
         const int r = 4 * half + ((lane & 15) >> 2);
         const int u = 4 * c + 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1);
-        v_rd[c] = kBuf + r * kRow + 16 * (u ^ v_swz<D>(r)) + 8 * (lane & 1);
+        v_rd[c] = 2 * kBuf + r * kRow + 16 * (u ^ v_swz<D>(r)) + 8 * (lane & 1);
     }
 
-    f32x16 o[kTiles] = {};
-    float m = kLowest, l = 0.f;
+    f32x16 o[RT][kTiles] = {}, x[RT][2];
+    float m[RT], l[RT];
+#pragma unroll
+    for (int r = 0; r < RT; ++r)
+        m[r] = kLowest, l[r] = 0.f;
 
-    auto compute = [&](int t, const uint8_t *buf, bool masked, bool bad) {
-        f32x16 x[2] = {};
+    // element i of x[r][sub] is the score of key 64 t + 32 sub + 8 (i / 4) + 4 half + i % 4
+    auto scores = [&](int t, f32x16 (&y)[RT][2]) {
+        const uint8_t *const buf = lds + (t & 1) * kBuf;
+#pragma unroll
+        for (int r = 0; r < RT; ++r)
+            y[r][0] = f32x16{}, y[r][1] = f32x16{};
 #pragma unroll
         for (int s = 0; s < kSteps; ++s)
 #pragma unroll
-            for (int sub = 0; sub < 2; ++sub)
-                x[sub] = mfma32x32x16<F16>(*reinterpret_cast<const u32x4 *>(buf + k_rd[s] + 32 * kRow * sub), q[s], x[sub]);
-        // row i of x[sub] is key 32 sub + 8 (i / 4) + 4 half + i % 4
-        const int left = seen - kKeys * t - 4 * half; // visible keys from this lane's first on
-        if (masked) {
+            for (int sub = 0; sub < 2; ++sub) {
+                const u32x4 k = *reinterpret_cast<const u32x4 *>(buf + k_rd[s] + 32 * kRow * sub);
 #pragma unroll
-            for (int sub = 0; sub < 2; ++sub)
+                for (int r = 0; r < RT; ++r)
+                    y[r][sub] = mfma32x32x16<F16>(k, q[r][s], y[r][sub]);
+            }
+    };
+    auto hide = [&](int t, f32x16 (&y)[RT][2]) {
 #pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    if (32 * sub + 8 * (i >> 2) + (i & 3) >= left)
-                        x[sub][i] = -INFINITY;
+        for (int r = 0; r < RT; ++r) {
+            const int left = seen[r] - kKeys * t - 4 * half; // visible keys from this lane's first on
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+                if (32 * (i >> 4) + 8 * ((i & 15) >> 2) + (i & 3) >= left)
+                    y[r][i >> 4][i & 15] = -INFINITY;
         }
-        float top = x[0][0];
+    };
+    auto highest = [&](const f32x16 (&y)[RT][2], float (&top)[RT]) {
 #pragma unroll
-        for (int i = 1; i < 32; ++i)
-            top = fmaxf(top, x[i >> 4][i & 15]);
-        top = max_swap32(top) * a.scale_log2 - kHeadroom<F16>;
-        if (__builtin_amdgcn_ballot_w64(top > m + kRescaleSlack)) {
-            const float to = fmaxf(m, top), f = exp2_fast(m - to);
-            m = to;
-            l *= f;
+        for (int r = 0; r < RT; ++r) {
+            float t0 = y[r][0][0], t1 = y[r][1][0];
+#pragma unroll
+            for (int i = 1; i < 15; i += 2) {
+                t0 = fmaxf(fmaxf(t0, y[r][0][i]), y[r][0][i + 1]);
+                t1 = fmaxf(fmaxf(t1, y[r][1][i]), y[r][1][i + 1]);
+            }
+            t0 = fmaxf(fmaxf(t0, y[r][0][15]), t1);
+            top[r] = max_swap32(fmaxf(t0, y[r][1][15])) * a.scale_log2 - kHeadroom<F16>;
+        }
+    };
+    auto raise = [&](const float (&top)[RT]) {
+        bool grows = false;
+#pragma unroll
+        for (int r = 0; r < RT; ++r)
+            grows |= top[r] > m[r] + kRescaleSlack;
+        if (__builtin_amdgcn_ballot_w64(grows)) {
+#pragma unroll
+            for (int r = 0; r < RT; ++r) {
+                const float to = fmaxf(m[r], top[r]), f = exp2_fast(m[r] - to);
+                m[r] = to;
+                l[r] *= f;
+#pragma unroll
+                for (int c = 0; c < kTiles; ++c)
+                    o[r][c] *= f;
+            }
+        }
+    };
+    // An infinity or NaN in V at a key that some rows do not see: 0 V would
+    // spoil them.  Rows that see it take it here, lane by lane; then it is
+    // zeroed in LDS.  Rare: one lane's 4 channels at a time.
+    auto mend = [&](int t) {
+        uint8_t *const buf = lds + (2 + (t & 1)) * kBuf;
+#pragma unroll 1
+        for (int key = 0; key < kKeys; ++key)
 #pragma unroll
             for (int c = 0; c < kTiles; ++c)
-                o[c] *= f;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) { // channels 32 c + 8 i + 4 half ..
+                    const int unit = 4 * c + i;
+                    const u32x2 v = *reinterpret_cast<const u32x2 *>(buf + key * kRow + 16 * (unit ^ v_swz<D>(key)) + 8 * half);
+                    if (nonfinite_halves<F16>(v[0]) | nonfinite_halves<F16>(v[1])) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const uint32_t b = v[e >> 1] >> (16 * (e & 1)) & 0xFFFFu;
+                            const bool odd = nonfinite_halves<F16>(b) != 0;
+#pragma unroll
+                            for (int r = 0; r < RT; ++r)
+                                o[r][c][4 * i + e] += odd && kKeys * t + key < seen[r] ? half_bits_to_f32<F16>(b) : 0.f;
+                        }
+                    }
+                }
+        wait_lgkmcnt0();
+        lds_barrier();
+#pragma unroll 1
+        for (int i = 0; i < kDmas; ++i) { // this wave's rows
+            u32x4 *const p = reinterpret_cast<u32x4 *>(buf + 16 * wave * kRow + 1024 * i + 16 * lane);
+            u32x4 v = *p;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const uint32_t bad = nonfinite_halves<F16>(v[j]);
+                v[j] &= ~((bad & 0x8000u ? 0xFFFFu : 0u) | (bad & 0x80000000u ? 0xFFFF0000u : 0u));
+            }
+            *p = v;
         }
-        // P rounds to the inputs' type (nearest even) for the MFMA; the sum is
-        // kept in fp32 over the unrounded values
-        u32x4 p[4];
-        float sum = 0.f;
+        wait_lgkmcnt0();
+        lds_barrier();
+    };
+
+    // Tile t: p from its scores x, while the products of the next tile's
+    // scores run; then P V, while the next scores' maximum is taken.
+    auto step = [&](int t, auto more, auto masked) {
+        f32x16 y[RT][2];
+        u32x4 p[RT][4];
+        if constexpr (more)
+            scores(t + 1, y);
 #pragma unroll
-        for (int i = 0; i < 32; i += 2) {
-            const float e0 = exp2_fast(x[i >> 4][i & 15] * a.scale_log2 - m);
-            const float e1 = exp2_fast(x[i >> 4][(i & 15) + 1] * a.scale_log2 - m);
-            sum += e0 + e1;
-            p[i >> 3][(i & 7) >> 1] = pack_half_x2<F16>(e0, e1);
-        }
-        l += sum;
+        for (int r = 0; r < RT; ++r)
 #pragma unroll
-        for (int c = 0; c < kTiles; ++c)
+            for (int i = 0; i < 32; i += 2) {
+                const uint32_t w = pack_half_x2<F16>(exp2_fast(x[r][i >> 4][i & 15] * a.scale_log2 - m[r]),
+                                                     exp2_fast(x[r][i >> 4][(i & 15) + 1] * a.scale_log2 - m[r]));
+                p[r][i >> 3][(i & 7) >> 1] = w;
+                l[r] = dot_ones<F16>(w, l[r]);
+            }
+        if constexpr (more && masked)
+            hide(t + 1, y);
+        float top[RT];
+        if constexpr (more)
+            highest(y, top);
+        const uint8_t *const buf = lds + (t & 1) * kBuf;
 #pragma unroll
-            for (int ks = 0; ks < 4; ++ks) {
+        for (int ks = 0; ks < 4; ++ks)
+#pragma unroll
+            for (int c = 0; c < kTiles; ++c) {
                 const u32x2 lo = lds_read_tr(buf + v_rd[c] + 16 * ks * kRow);
                 const u32x2 hi = lds_read_tr(buf + v_rd[c] + (16 * ks + 8) * kRow);
-                u32x4 v = {lo[0], lo[1], hi[0], hi[1]};
-                if (masked && bad) {
-                    // An infinity or NaN in this tile of V, at a key that some rows
-                    // may not see: 0 V would spoil them.  Multiply with V's finite
-                    // values, and add each kind of non-finite value where a row
-                    // sees one (counted by a product of truth values).
-                    u32x4 vis;
+                const u32x4 v = {lo[0], lo[1], hi[0], hi[1]};
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const int key = 16 * ks + 8 * (j >> 1) + 2 * (j & 1);
-                        const uint32_t one = F16 ? 0x3C00u : 0x3F80u;
-                        vis[j] = (key < left ? one : 0u) | (key + 1 < left ? one << 16 : 0u);
-                    }
-                    u32x4 fin = v;
-#pragma unroll 1
-                    for (int kind = 0; kind < 3; ++kind) {
-                        u32x4 is = {};
-#pragma unroll
-                        for (int j = 0; j < 4; ++j)
-#pragma unroll
-                            for (int e = 0; e < 32; e += 16) {
-                                const uint32_t b = (v[j] >> e) & 0xFFFFu, inf = F16 ? 0x7C00u : 0x7F80u;
-                                if (kind == 0 ? b == inf : kind == 1 ? b == (inf | 0x8000u) : (b & 0x7FFFu) > inf) {
-                                    is[j] |= (F16 ? 0x3C00u : 0x3F80u) << e;
-                                    fin[j] &= ~(0xFFFFu << e);
-                                }
-                            }
-                        const float add = kind == 0 ? INFINITY : kind == 1 ? -INFINITY : NAN;
-                        const f32x16 seen_of = mfma32x32x16<F16>(is, vis, f32x16{});
-#pragma unroll
-                        for (int i = 0; i < 16; ++i)
-                            o[c][i] += seen_of[i] > 0.f ? add : 0.f;
-                    }
-                    o[c] = mfma32x32x16<F16>(fin, p[ks], o[c]);
-                } else {
-                    o[c] = mfma32x32x16<F16>(v, p[ks], o[c]);
-                }
+                for (int r = 0; r < RT; ++r)
+                    o[r][c] = mfma32x32x16<F16>(v, p[r][ks], o[r][c]);
             }
+        if constexpr (more) {
+            raise(top);
+#pragma unroll
+            for (int r = 0; r < RT; ++r)
+                x[r][0] = y[r][0], x[r][1] = y[r][1];
+        }
     };
 
     if (tiles > 0) {
-        fetch(0, 0, page_of(0));
-        int next_page = page_of(1);
-        for (int t = 0; t < tiles; ++t) {
-            uint8_t *const buf = lds + 2 * (t & 1) * kBuf;
-            const bool masked = kKeys * (t + 1) > seen_first;
-            wait_vmcnt<0>(); // the wave's copies of tile t
-            if (masked) {
-                // does V of this tile hold anything but finite numbers?
+        fetch(true, 0, page_of(0));
+        fetch(false, 0, page_of(0));
+        fetch(true, 1, page_of(1));
+        int next_page = page_of(1), far_page = page_of(2);
+        wait_vmcnt<2 * kDmas>(); // the wave's copies of the first keys
+        lds_barrier();
+        scores(0, x);
+        if (whole == 0)
+            hide(0, x);
+        float top[RT];
+        highest(x, top);
+        raise(top);
+        // Before tile t: its values and the next tile's keys are there for
+        // everybody, and the buffers of the values before and of its own keys
+        // are used up.
+        auto turn = [&](int t, auto check) {
+            wait_vmcnt<0>();
+            asm volatile("" ::: "memory"); // no read of LDS moves above the wait
+            if constexpr (check) {
                 uint32_t w = 0;
 #pragma unroll
                 for (int i = 0; i < kDmas; ++i) {
-                    const u32x4 v = *reinterpret_cast<const u32x4 *>(buf + kBuf + 16 * wave * kRow + 1024 * i + 16 * lane);
+                    const u32x4 v = *reinterpret_cast<const u32x4 *>(lds + (2 + (t & 1)) * kBuf + 16 * wave * kRow + 1024 * i + 16 * lane);
                     w |= nonfinite_halves<F16>(v[0]) | nonfinite_halves<F16>(v[1]) | nonfinite_halves<F16>(v[2]) |
                          nonfinite_halves<F16>(v[3]);
                 }
                 const bool any = __builtin_amdgcn_ballot_w64(w != 0) != 0;
                 if (lane == 0)
-                    s_bad[wave] = any;
+                    s_bad[t & 1][wave] = any;
                 wait_lgkmcnt0();
             }
-            lds_barrier(); // everybody's copies are there, and tile t - 1 is used up
+            lds_barrier();
+            if (t + 2 < tiles)
+                fetch(true, t + 2, far_page);
             if (t + 1 < tiles)
-                fetch(t + 1, (t + 1) & 1, next_page);
-            next_page = page_of(t + 2);
-            if (masked) {
-                const bool bad = s_bad[0] | s_bad[1] | s_bad[2] | s_bad[3];
+                fetch(false, t + 1, next_page);
+            next_page = far_page;
+            far_page = page_of(t + 3);
+            if constexpr (check) {
+                const uint32_t bad = s_bad[t & 1][0] | s_bad[t & 1][1] | s_bad[t & 1][2] | s_bad[t & 1][3];
                 if (__builtin_amdgcn_readfirstlane((int)bad))
-                    compute(t, buf, true, true);
-                else
-                    compute(t, buf, true, false);
-                if (t + 1 < tiles)
-                    lds_barrier(); // s_bad is read before the next tile writes it
-            } else {
-                compute(t, buf, false, false);
+                    mend(t);
             }
+        };
+        int t = 0;
+        for (; t + 1 < whole && t + 1 < tiles; ++t) {
+            turn(t, std::false_type{});
+            step(t, std::true_type{}, std::false_type{});
         }
+        for (; t + 1 < tiles; ++t) {
+            turn(t, std::true_type{});
+            step(t, std::true_type{}, std::true_type{});
+        }
+        turn(t, std::true_type{});
+        step(t, std::false_type{}, std::true_type{});
     }
 
-    l = sum_swap32(l);
-    const float inv = l == 0.f ? 1.f : 1.f / l;
-    if (row < rows) {
-        uint16_t *const p = a.out + ((int64_t)(q0 + token) * a.hkv * a.G + head) * D + 4 * half;
 #pragma unroll
-        for (int c = 0; c < kTiles; ++c)
+    for (int r = 0; r < RT; ++r) {
+        const float sum = sum_swap32(l[r]);
+        const float inv = sum == 0.f ? 1.f : 1.f / sum;
+        if (row[r] < rows) {
 #pragma unroll
-            for (int i = 0; i < 16; i += 4) {
-                const u32x2 w = {pack_half_x2<F16>(o[c][i] * inv, o[c][i + 1] * inv),
-                                 pack_half_x2<F16>(o[c][i + 2] * inv, o[c][i + 3] * inv)};
-                *reinterpret_cast<u32x2 *>(p + 32 * c + 2 * i) = w;
-            }
+            for (int c = 0; c < kTiles; ++c)
+#pragma unroll
+                for (int i = 0; i < 16; i += 4) {
+                    const u32x2 w = {pack_half_x2<F16>(o[r][c][i] * inv, o[r][c][i + 1] * inv),
+                                     pack_half_x2<F16>(o[r][c][i + 2] * inv, o[r][c][i + 3] * inv)};
+                    *reinterpret_cast<u32x2 *>(a.out + at_out[r] + 32 * c + 2 * i) = w;
+                }
+        }
     }
 }
 
 template <int D, bool F16, bool PAGED> hipError_t run(const PrefillArgs &a, int64_t seqs, hipStream_t st)
 {
-    const int64_t tiles = ((int64_t)a.longest * a.G + kRowsBlock - 1) / kRowsBlock;
-    attn_prefill_kernel<D, F16, PAGED><<<dim3((unsigned)(a.hkv * seqs), (unsigned)tiles), 64 * kWaves, 0, st>>>(a);
+    constexpr int RT = PF_RT;
+    const int64_t tiles = ((int64_t)a.longest * a.G + 128 * RT - 1) / (128 * RT);
+    attn_prefill_kernel<D, F16, PAGED, RT><<<dim3((unsigned)(a.hkv * seqs), (unsigned)tiles), 64 * kWaves, 8 * kKeys * D, st>>>(a);
     return hipGetLastError();
 }
 

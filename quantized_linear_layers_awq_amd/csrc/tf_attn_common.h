@@ -55,6 +55,7 @@ __device__ __forceinline__ float sum_swap32(float x)
 // LDS transpose read: in each group of 16 lanes, lane i supplies the address
 // of 4 consecutive 16-bit values; lanes 4 r .. 4 r + 3 together name row r of
 // a 4 x 16 matrix, and lane j receives its column j (rows 0..3).
+typedef short s16x2 __attribute__((ext_vector_type(2)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 __device__ __forceinline__ u32x2 lds_read_tr(const uint8_t *p)
 {

@@ -103,18 +103,24 @@ int tf_attn_decode(int type, const uint16_t *q, int64_t q_token, int64_t q_head,
  *   longest  an upper bound of the new tokens of a sequence (tokens past it
  *          are not computed), at most T
  *   out    [T][Hq][D]; rows of no sequence are not written
- * T and keys are at most 2^30. */
+ * T and keys are at most 2^30.  The workspace holds partial results where few
+ * rows meet many keys and the keys are cut into ranges; the size depends on
+ * the device's compute units, results do not depend on what it held. */
+size_t tf_attn_prefill_workspace_bytes(int64_t seqs, int64_t T, int64_t Hq, int64_t Hkv, int64_t D, int64_t longest,
+                                       int64_t keys);
 int tf_attn_prefill(int type, const uint16_t *q, int64_t q_token, int64_t q_head, const uint16_t *k, int64_t k_token,
                     int64_t k_head, const uint16_t *v, int64_t v_token, int64_t v_head, const int32_t *cu_q,
                     const int32_t *cu_k, uint16_t *out, int64_t seqs, int64_t T, int64_t keys, int64_t Hq, int64_t Hkv,
-                    int64_t D, int64_t longest, float scale, void *stream);
+                    int64_t D, int64_t longest, float scale, void *workspace, size_t ws_bytes, void *stream);
 
 /* The same over the pages of a cache that already holds the sequences' lens[s]
- * tokens, the new ones included (prompts in chunks, shared prefixes). */
+ * tokens, the new ones included (prompts in chunks, shared prefixes).  `keys`
+ * of the workspace's size is width * page. */
 int tf_attn_prefill_paged(int type, const uint16_t *q, int64_t q_token, int64_t q_head, const uint16_t *k_pages,
                           const uint16_t *v_pages, int64_t pages, int64_t page, const int32_t *tables, int64_t width,
                           const int32_t *cu_q, const int32_t *lens, uint16_t *out, int64_t seqs, int64_t T, int64_t Hq,
-                          int64_t Hkv, int64_t D, int64_t longest, float scale, void *stream);
+                          int64_t Hkv, int64_t D, int64_t longest, float scale, void *workspace, size_t ws_bytes,
+                          void *stream);
 
 /* ------------------------------------------------------------------------ */
 /* The pool.  refs int32 [pages] counts the table entries that name a page;  */

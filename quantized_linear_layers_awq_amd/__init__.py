@@ -67,6 +67,7 @@ from ._attention import (  # noqa: F401
     tf_attn_decode_workspace_bytes,
     tf_attn_prefill,
     tf_attn_prefill_paged,
+    tf_attn_prefill_workspace_bytes,
     tf_kv_append,
     tf_kv_compact,
     tf_kv_compact_workspace_bytes,

@@ -175,7 +175,11 @@ def tf_attn_decode(q, k_pages, v_pages, tables, lens, longest, scale=None, out=N
     return out
 
 
-def tf_attn_prefill(q, k, v, cu_q, cu_k, longest, scale=None, out=None, stream=None):
+def tf_attn_prefill_workspace_bytes(seqs: int, tokens: int, hq: int, hkv: int, d: int, longest: int, keys: int) -> int:
+    return int(load_library().tf_attn_prefill_workspace_bytes(seqs, tokens, hq, hkv, d, longest, keys))
+
+
+def tf_attn_prefill(q, k, v, cu_q, cu_k, longest, scale=None, out=None, workspace=None, stream=None):
     """Causal attention of packed prompts: q [T][Hq][D], k and v
     [keys][Hkv][D] (channels contiguous; parts of one fused QKV output will
     do), sequence s in rows cu_q[s] .. cu_q[s + 1] of q and cu_k[s] ..
@@ -196,15 +200,19 @@ def tf_attn_prefill(q, k, v, cu_q, cu_k, longest, scale=None, out=None, stream=N
     qt, qh = _stride(q, fn, "q")
     kt, kh = _stride(k, fn, "k")
     vt, vh = _stride(v, fn, "v")
+    lib, seqs = _lib(), cu_q.numel() - 1
     with _On(device, stream) as on:
         out = _result(out, (tokens, hq, d), q.dtype, device, fn, "out")
-        _check(_lib().tf_attn_prefill(kind, q.data_ptr(), qt, qh, k.data_ptr(), kt, kh, v.data_ptr(), vt, vh,
-                                      cu_q.data_ptr(), cu_k.data_ptr(), out.data_ptr(), cu_q.numel() - 1, tokens, keys,
-                                      hq, hkv, d, longest, _scale(scale, d), on.handle), fn)
+        ws, have = _need_workspace(workspace, device, on.handle,
+                                   lib.tf_attn_prefill_workspace_bytes(seqs, tokens, hq, hkv, d, longest, keys), fn)
+        _check(lib.tf_attn_prefill(kind, q.data_ptr(), qt, qh, k.data_ptr(), kt, kh, v.data_ptr(), vt, vh,
+                                      cu_q.data_ptr(), cu_k.data_ptr(), out.data_ptr(), seqs, tokens, keys, hq, hkv, d,
+                                   longest, _scale(scale, d), ws, have, on.handle), fn)
     return out
 
 
-def tf_attn_prefill_paged(q, k_pages, v_pages, tables, cu_q, lens, longest, scale=None, out=None, stream=None):
+def tf_attn_prefill_paged(q, k_pages, v_pages, tables, cu_q, lens, longest, scale=None, out=None, workspace=None,
+                          stream=None):
     """Causal attention of packed new tokens q [T][Hq][D] (sequence s in rows
     cu_q[s] .. cu_q[s + 1]) over the first lens[s] tokens of the sequences'
     pages, the new ones included.  Returns [T][Hq][D]."""
@@ -220,12 +228,15 @@ def tf_attn_prefill_paged(q, k_pages, v_pages, tables, cu_q, lens, longest, scal
         raise ValueError(f"{fn}: cu_q must have {seqs + 1} entries, tables {seqs} rows")
     tokens, hq, _ = q.shape
     token, head = _stride(q, fn, "q")
+    lib, width = _lib(), tables.shape[1]
     with _On(device, stream) as on:
         out = _result(out, (tokens, hq, d), q.dtype, device, fn, "out")
-        _check(_lib().tf_attn_prefill_paged(kind, q.data_ptr(), token, head, k_pages.data_ptr(), v_pages.data_ptr(),
-                                            pages, page, tables.data_ptr(), tables.shape[1], cu_q.data_ptr(),
-                                            lens.data_ptr(), out.data_ptr(), seqs, tokens, hq, hkv, d, longest,
-                                            _scale(scale, d), on.handle), fn)
+        ws, have = _need_workspace(workspace, device, on.handle,
+                                   lib.tf_attn_prefill_workspace_bytes(seqs, tokens, hq, hkv, d, longest, width * page), fn)
+        _check(lib.tf_attn_prefill_paged(kind, q.data_ptr(), token, head, k_pages.data_ptr(), v_pages.data_ptr(),
+                                            pages, page, tables.data_ptr(), width, cu_q.data_ptr(), lens.data_ptr(),
+                                         out.data_ptr(), seqs, tokens, hq, hkv, d, longest, _scale(scale, d), ws, have,
+                                         on.handle), fn)
     return out
 
 

@@ -91,9 +91,10 @@ def load_library():
         L.tf_attn_decode_workspace_bytes.argtypes = [I64] * 5
         L.tf_attn_decode.argtypes = [I, P, I64, I64, P, P, I64, I64, P, I64, P, P, I64, I64, I64, I64, I64, F, P, SZ, P]
         L.tf_attn_prefill.argtypes = [I, P, I64, I64, P, I64, I64, P, I64, I64, P, P, P, I64, I64, I64, I64, I64, I64,
-                                      I64, F, P]
+                                      I64, F, P, SZ, P]
         L.tf_attn_prefill_paged.argtypes = [I, P, I64, I64, P, P, I64, I64, P, I64, P, P, P, I64, I64, I64, I64, I64, I64,
-                                            F, P]
+                                            F, P, SZ, P]
+        L.tf_attn_prefill_workspace_bytes.argtypes = [I64] * 7
         L.tf_kv_fork_workspace_bytes.argtypes = [I64]
         L.tf_kv_fork.argtypes = [P, I64, I64, I64, I64, I64, P, P, P, I64, I64, P, P, I64, P, P, P, P, P, SZ, P]
         L.tf_kv_compact_workspace_bytes.argtypes = [I64]
@@ -101,7 +102,7 @@ def load_library():
         for n in ("tf_kv_append", "tf_attn_decode", "tf_attn_prefill", "tf_attn_prefill_paged", "tf_kv_fork",
                   "tf_kv_compact"):
             getattr(L, n).restype = I
-        for n in ("tf_attn_decode_workspace_bytes", "tf_kv_fork_workspace_bytes", "tf_kv_compact_workspace_bytes"):
+        for n in ("tf_attn_decode_workspace_bytes", "tf_attn_prefill_workspace_bytes", "tf_kv_fork_workspace_bytes", "tf_kv_compact_workspace_bytes"):
             getattr(L, n).restype = SZ
         _lib = L
         return _lib

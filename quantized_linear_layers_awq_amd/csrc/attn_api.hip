@@ -12,7 +12,7 @@ namespace {
 constexpr int64_t kIntLimit = int64_t(1) << 31;
 constexpr int64_t kKeyLimit = int64_t(1) << 30; // key numbers, and a few tiles past the last, are 32-bit
 constexpr int64_t kStrideLimit = int64_t(1) << 26; // 16 rows of a strided tensor within 31-bit byte offsets
-constexpr int64_t kGridYZ = 65535;
+constexpr int64_t kGridYZ = 65535; // sequences of a decode call, a grid axis
 constexpr int kMaxGroup = 1024;
 
 bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
@@ -82,28 +82,52 @@ int check_decode_sizes(int type, int64_t seqs, int64_t Hq, int64_t Hkv, int64_t 
     return seqs >= 0 && seqs <= kGridYZ && seqs * Hq < kIntLimit && longest >= 0 && longest <= kKeyLimit ? TF_OK : TF_ERR_SHAPE;
 }
 
-int prefill(int type, tf::PrefillArgs &a, int64_t D, bool paged, int64_t seqs, void *stream)
+int check_ws(const void *ws, size_t have, size_t need)
 {
+    if (!need)
+        return TF_OK;
+    if (!ws)
+        return TF_ERR_NULL;
+    if (!aligned(ws, 256))
+        return TF_ERR_ALIGN;
+    return have < need ? TF_ERR_BUFFER_TOO_SMALL : TF_OK;
+}
+
+// Floats of the partial results of a prefill call of valid sizes.
+int64_t prefill_part_floats(int64_t T, int64_t Hq, int64_t D, int splits) { return splits > 1 ? T * Hq * splits * (D + 2) : 0; }
+
+int prefill(int type, tf::PrefillArgs &a, int64_t Hq, int64_t D, bool paged, int64_t seqs, int64_t keys, void *ws,
+            size_t ws_bytes, void *stream)
+{
+    a.seqs = (int)seqs;
+    a.splits = tf::plan_prefill_splits(seqs, a.tokens, a.hkv, a.G, a.longest, keys, tf::device_cus());
+    const int64_t floats = prefill_part_floats(a.tokens, Hq, D, a.splits);
+    if (int st = check_ws(ws, ws_bytes, (size_t)floats * sizeof(float)))
+        return st;
+    a.part = static_cast<float *>(ws);
+    a.stats = floats ? a.part + (int64_t)a.tokens * Hq * a.splits * D : nullptr;
     return tf::launch_attn_prefill(a, (int)D, type == TF_TYPE_F16, paged, seqs, static_cast<hipStream_t>(stream)) ==
                    hipSuccess
                ? TF_OK
                : TF_ERR_HIP;
 }
 
-// What both prefill calls ask of their queries.
-int check_queries(int type, const uint16_t *q, int64_t q_token, int64_t q_head, const int32_t *cu_q, const uint16_t *out,
-                  int64_t seqs, int64_t T, int64_t Hq, int64_t Hkv, int64_t D, int64_t longest, float scale)
+// Sizes of a prefill call.
+int check_prefill_sizes(int type, int64_t seqs, int64_t T, int64_t Hq, int64_t Hkv, int64_t D, int64_t longest, int64_t keys)
 {
     if (int st = check_heads(type, Hq, Hkv, D))
         return st;
-    if (!count_ok(seqs, 0) || T < 0 || T > kKeyLimit || longest < 0 || longest > T || seqs * Hkv >= kIntLimit)
+    if (!count_ok(seqs, 0) || T < 0 || T > kKeyLimit || longest < 0 || longest > T || keys < 0 || keys > kKeyLimit)
         return TF_ERR_SHAPE;
-    if (longest * (Hq / Hkv) > kGridYZ * 128) // workgroups along the rows
-        return TF_ERR_SHAPE;
-    if (!scale_ok(scale))
-        return TF_ERR_UNSUPPORTED;
-    if (seqs == 0 || T == 0 || longest == 0)
-        return TF_OK;
+    // workgroups: at most twice the sequences' (in bundles), times the ranges of keys of a small call
+    const int64_t blocks = std::max<int64_t>(1, tf::prefill_blocks(longest, Hq / Hkv)) * Hkv; // of a sequence: < 2^50
+    return seqs && blocks > (kIntLimit - 1) / 2 / seqs ? TF_ERR_SHAPE : TF_OK;
+}
+
+// What both prefill calls ask of their queries.
+int check_queries(const uint16_t *q, int64_t q_token, int64_t q_head, const int32_t *cu_q, const uint16_t *out, int64_t Hq,
+                  int64_t D)
+{
     if (!cu_q || !out)
         return TF_ERR_NULL;
     if (!aligned(cu_q, 4) || !aligned(out, 16))
@@ -127,17 +151,6 @@ int check_pool(uint16_t *cache, int64_t planes, int64_t pages, int64_t Hkv, int6
         !aligned(told, 4))
         return TF_ERR_ALIGN;
     return TF_OK;
-}
-
-int check_ws(const void *ws, size_t have, size_t need)
-{
-    if (!need)
-        return TF_OK;
-    if (!ws)
-        return TF_ERR_NULL;
-    if (!aligned(ws, 256))
-        return TF_ERR_ALIGN;
-    return have < need ? TF_ERR_BUFFER_TOO_SMALL : TF_OK;
 }
 
 size_t fork_ws(int64_t forks) { return forks > 0 ? (size_t)forks * 4 * sizeof(int32_t) : 0; }
@@ -239,17 +252,28 @@ int tf_attn_decode(int type, const uint16_t *q, int64_t q_token, int64_t q_head,
                : TF_ERR_HIP;
 }
 
+size_t tf_attn_prefill_workspace_bytes(int64_t seqs, int64_t T, int64_t Hq, int64_t Hkv, int64_t D, int64_t longest,
+                                       int64_t keys)
+{
+    if (check_prefill_sizes(TF_TYPE_BF16, seqs, T, Hq, Hkv, D, longest, keys) != TF_OK || seqs == 0 || T == 0 || longest == 0)
+        return 0;
+    const int splits = tf::plan_prefill_splits(seqs, T, Hkv, Hq / Hkv, longest, keys, tf::device_cus());
+    return (size_t)prefill_part_floats(T, Hq, D, splits) * sizeof(float);
+}
+
 int tf_attn_prefill(int type, const uint16_t *q, int64_t q_token, int64_t q_head, const uint16_t *k, int64_t k_token,
                     int64_t k_head, const uint16_t *v, int64_t v_token, int64_t v_head, const int32_t *cu_q,
                     const int32_t *cu_k, uint16_t *out, int64_t seqs, int64_t T, int64_t keys, int64_t Hq, int64_t Hkv,
-                    int64_t D, int64_t longest, float scale, void *stream)
+                    int64_t D, int64_t longest, float scale, void *workspace, size_t ws_bytes, void *stream)
 {
-    if (int st = check_queries(type, q, q_token, q_head, cu_q, out, seqs, T, Hq, Hkv, D, longest, scale))
+    if (int st = check_prefill_sizes(type, seqs, T, Hq, Hkv, D, longest, keys))
         return st;
-    if (keys < 0 || keys > kKeyLimit)
-        return TF_ERR_SHAPE;
+    if (!scale_ok(scale))
+        return TF_ERR_UNSUPPORTED;
     if (seqs == 0 || T == 0 || longest == 0)
         return TF_OK;
+    if (int st = check_queries(q, q_token, q_head, cu_q, out, Hq, D))
+        return st;
     if (!cu_k)
         return TF_ERR_NULL;
     if (!aligned(cu_k, 4))
@@ -279,18 +303,23 @@ int tf_attn_prefill(int type, const uint16_t *q, int64_t q_token, int64_t q_head
     a.G = (int)(Hq / Hkv);
     a.longest = (int)longest;
     a.scale_log2 = scale * kLog2E;
-    return prefill(type, a, D, false, seqs, stream);
+    return prefill(type, a, Hq, D, false, seqs, keys, workspace, ws_bytes, stream);
 }
 
 int tf_attn_prefill_paged(int type, const uint16_t *q, int64_t q_token, int64_t q_head, const uint16_t *k_pages,
                           const uint16_t *v_pages, int64_t pages, int64_t page, const int32_t *tables, int64_t width,
                           const int32_t *cu_q, const int32_t *lens, uint16_t *out, int64_t seqs, int64_t T, int64_t Hq,
-                          int64_t Hkv, int64_t D, int64_t longest, float scale, void *stream)
+                          int64_t Hkv, int64_t D, int64_t longest, float scale, void *workspace, size_t ws_bytes,
+                          void *stream)
 {
-    if (int st = check_queries(type, q, q_token, q_head, cu_q, out, seqs, T, Hq, Hkv, D, longest, scale))
+    if (int st = check_prefill_sizes(type, seqs, T, Hq, Hkv, D, longest, 0))
         return st;
+    if (!scale_ok(scale))
+        return TF_ERR_UNSUPPORTED;
     if (seqs == 0 || T == 0 || longest == 0)
         return TF_OK;
+    if (int st = check_queries(q, q_token, q_head, cu_q, out, Hq, D))
+        return st;
     if (!lens)
         return TF_ERR_NULL;
     if (!aligned(lens, 4))
@@ -310,7 +339,7 @@ int tf_attn_prefill_paged(int type, const uint16_t *q, int64_t q_token, int64_t 
     a.G = (int)(Hq / Hkv);
     a.longest = (int)longest;
     a.scale_log2 = scale * kLog2E;
-    return prefill(type, a, D, true, seqs, stream);
+    return prefill(type, a, Hq, D, true, seqs, width * page, workspace, ws_bytes, stream);
 }
 
 size_t tf_kv_fork_workspace_bytes(int64_t forks) { return count_ok(forks, 0) ? fork_ws(forks) : 0; }

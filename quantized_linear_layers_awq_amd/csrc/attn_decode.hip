@@ -90,7 +90,7 @@ template <int D, bool F16, int NT> __global__ __launch_bounds__(64 * kWaves, 2) 
         for (int sub = 0; sub < 2; ++sub) {
             const int key = key0 + 16 * sub;
             const int id = __builtin_amdgcn_readlane(ids, (2 * it + sub) & 63);
-            const int rows = id < 0 ? 0 : clampi(c1 - key, 0, 16);
+            const int rows = id < 0 ? 0 : rows_before(c1, key);
             const int64_t at = ((int64_t)max(id, 0) * a.cache.hkv + h) * page_elems + (int64_t)(key & page_mask) * D;
             const Rsrc kr = make_rsrc_n(a.cache.k + at, rows * kRow), vr = make_rsrc_n(a.cache.v + at, rows * kRow);
 #pragma unroll

@@ -22,9 +22,12 @@
 //    transpose reads do.
 //  - Wave w copies rows 16 w .. 16 w + 15, which lie in one page (pages hold a
 //    multiple of 16 tokens): one page id per wave and tile.
-//  - Workgroups are ordered with the last rows first (they see the most keys),
-//    and with the key-value head fastest, so that an XCD's L2 serves the same
-//    heads throughout.
+//  - Workgroups that run side by side share keys and values in their XCD's L2:
+//    they are ordered by bundles of sequences and heads that fit there, and in
+//    a bundle with the last rows first, which see the most keys (four
+//    sequences of up to 6000 tokens, 64/8 heads: 601 us, and 1029 with all
+//    four side by side).
+//  - Few rows behind many keys: the keys are cut into ranges and joined.
 #include "tf_attn.h"
 
 namespace tf {
@@ -33,9 +36,18 @@ namespace {
 
 constexpr int kWaves = 4;
 constexpr int kKeys = 64;
+constexpr int kMinRange = 4;   // tiles of a range of keys, at least
+constexpr int kMaxSplits = 16; // ranges
+constexpr int64_t kL2Share = 3 << 20;
+
+// tiles of a range when the keys of a sequence are cut into `splits`
+__device__ __forceinline__ int prefill_range(int keys, int splits)
+{
+    return splits == 1 ? 1 << 30 : max(kMinRange, ((keys + kKeys - 1) / kKeys + splits - 1) / splits);
+}
 
 template <int D> __device__ constexpr int k_swz(int row) { return D == 128 ? row & 15 : (row >> 1) & 7; }
-template <int D> __device__ constexpr int v_swz(int row) { return D == 128 ? 2 * (row & 7) : 2 * ((row >> 1) & 3); }
+template <int D> __device__ constexpr int v_swz(int row) { return D == 128 ? 4 * (row & 3) : 4 * ((row >> 1) & 1); }
 
 // true where a 16-bit half has an exponent of all ones, at bit 15 / 31
 template <bool F16> __device__ __forceinline__ uint32_t nonfinite_halves(uint32_t w)
@@ -52,7 +64,7 @@ template <bool F16> __device__ __forceinline__ float dot_ones(uint32_t w, float 
         return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(s16x2, w), s16x2{0x3F80, 0x3F80}, acc, false);
 }
 
-template <int D, bool F16, bool PAGED, int RT> __global__ __launch_bounds__(64 * kWaves, RT == 2 ? 1 : 2) void attn_prefill_kernel(PrefillArgs a)
+template <int D, bool F16, bool PAGED> __global__ __launch_bounds__(64 * kWaves, 2) void attn_prefill_kernel(PrefillArgs a)
 {
     constexpr int kSteps = D / 16;          // MFMA steps over channels
     constexpr int kTiles = D / 32;          // 32-channel tiles of O^T
@@ -61,19 +73,26 @@ template <int D, bool F16, bool PAGED, int RT> __global__ __launch_bounds__(64 *
     constexpr int kRowsPerDma = 1024 / kRow;
     constexpr int kDmas = 16 / kRowsPerDma; // of a wave's 16 rows
     constexpr int kBuf = kKeys * kRow;
-    constexpr int kRowsBlock = kWaves * 32 * RT;
     extern __shared__ __attribute__((aligned(16))) uint8_t lds[]; // K, K, V, V
     __shared__ uint32_t s_bad[2][kWaves];
 
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int half = lane >> 5, n = lane & 31;
-    const int h = blockIdx.x % a.hkv, seq = blockIdx.x / a.hkv;
-    const int block = gridDim.y - 1 - blockIdx.y;
+    // bundle of sequences, group of heads, block of rows, sequence in the
+    // bundle, head in the group (fastest).  The sequences turn with the block,
+    // so that no XCD is left with the same ones throughout.
+    const int pairs = a.seqs_by * a.heads_by, groups = a.hkv / a.heads_by;
+    const int bundle = blockIdx.x / (a.blocks * pairs), rest = blockIdx.x % (a.blocks * pairs);
+    const int block = a.blocks - 1 - rest / pairs, pair = rest % pairs;
+    const int seq = bundle / groups * a.seqs_by + (pair / a.heads_by + block % a.seqs_by) % a.seqs_by;
+    const int h = bundle % groups * a.heads_by + pair % a.heads_by;
+    if (seq >= a.seqs)
+        return;
 
     const int q0 = clampi(a.cu_q[seq], 0, a.tokens);
     const int all_new = max(clampi(a.cu_q[seq + 1], 0, a.tokens) - q0, 0);
     const int fresh = min(all_new, a.longest); // tokens past the bound are not computed
-    const int64_t row0 = (int64_t)block * kRowsBlock;
+    const int64_t row0 = (int64_t)block * kPrefillRows;
     const int64_t rows = (int64_t)fresh * a.G;
     if (row0 >= rows)
         return;
@@ -87,25 +106,25 @@ template <int D, bool F16, bool PAGED, int RT> __global__ __launch_bounds__(64 *
     // keys visible to the first and the last token of the workgroup
     const int shift = keys - all_new + 1;
     const int seen_first = clampi(shift + (int)(row0 / a.G), 0, keys);
-    const int seen_last = clampi(shift + (int)((min(rows, row0 + kRowsBlock) - 1) / a.G), 0, keys);
-    const int tiles = (seen_last + kKeys - 1) / kKeys;
+    const int seen_last = clampi(shift + (int)((min(rows, row0 + kPrefillRows) - 1) / a.G), 0, keys);
     const int whole = seen_first / kKeys; // tiles that every row sees whole
+    // this workgroup's tiles: t0 .. tiles - 1
+    const int all_tiles = (seen_last + kKeys - 1) / kKeys, per = prefill_range(keys, a.splits);
+    const int split = blockIdx.y, t0 = split * per, tiles = min(all_tiles, t0 + per);
+    if (split > 0 && t0 >= all_tiles)
+        return; // the join reads only the ranges that a block has
 
-    // this lane's rows: token, head and visible keys
-    int64_t row[RT], at_out[RT];
-    int seen[RT];
-    u32x4 q[RT][kSteps];
-#pragma unroll
-    for (int r = 0; r < RT; ++r) {
-        row[r] = row0 + 32 * (RT * wave + r) + n;
-        const int64_t in = min(row[r], rows - 1);
-        const int token = (int)(in / a.G), head = h * a.G + (int)(in % a.G);
-        seen[r] = clampi(shift + token, 0, keys);
-        at_out[r] = ((int64_t)(q0 + token) * a.hkv * a.G + head) * D + 4 * half;
+    // this lane's row: token, head and visible keys
+    const int64_t row = row0 + 32 * wave + n, row_in = min(row, rows - 1);
+    const int token = (int)(row_in / a.G), head = h * a.G + (int)(row_in % a.G);
+    const int seen = clampi(shift + token, 0, keys);
+    const int64_t row_out = (int64_t)(q0 + token) * a.hkv * a.G + head;
+    u32x4 q[kSteps];
+    {
         const uint16_t *p = a.q + (int64_t)(q0 + token) * a.q_token + (int64_t)head * a.q_head + 8 * half;
 #pragma unroll
         for (int s = 0; s < kSteps; ++s)
-            q[r][s] = load16(p + 16 * s);
+            q[s] = load16(p + 16 * s);
     }
 
     // LDS-DMA of tile t: unit u of row i lands at u ^ swz(i)
@@ -119,19 +138,30 @@ template <int D, bool F16, bool PAGED, int RT> __global__ __launch_bounds__(64 *
         k_voff[i] = r * kstride + 16 * (d_unit ^ k_swz<D>(r));
         v_voff[i] = r * vstride + 16 * (d_unit ^ v_swz<D>(r));
     }
-    auto page_of = [&](int t) { // of the wave's rows of tile t; uniform
-        const int key = kKeys * t + 16 * wave;
-        return PAGED && key < keys ? table[key >> a.cache.page_shift] : -1;
+    // The pages of this wave's rows of 64 tiles, a lane per tile, in one load;
+    // a tile's page is read out of its lane, so that it is uniform.
+    int ids = -1;
+    auto pages_from = [&](int t) {
+        if constexpr (PAGED) {
+            const int key = kKeys * ((t & ~63) + lane) + 16 * wave;
+            ids = key < keys ? table[key >> a.cache.page_shift] : -1;
+            ids = ids < a.cache.pages ? ids : -1;
+        }
+    };
+    auto page_of = [&](int t) {
+        if constexpr (PAGED)
+            return __builtin_amdgcn_readlane(ids, t & 63);
+        else
+            return 0;
     };
     auto fetch = [&](bool is_k, int t, int page) {
         const int key = kKeys * t + 16 * wave;
-        const int have = clampi(keys - key, 0, 16);
+        const int have = rows_before(keys, key);
         const uint16_t *base = PAGED ? (is_k ? a.cache.k : a.cache.v) : is_k ? a.k : a.v;
         Rsrc rs;
         if constexpr (PAGED) {
-            const bool ok = page >= 0 && page < a.cache.pages;
-            const int64_t at = (((int64_t)(ok ? page : 0) * a.hkv + h) << a.cache.page_shift) + (key & ((1 << a.cache.page_shift) - 1));
-            rs = make_rsrc_n(base + at * D, ok ? have * kRow : 0);
+            const int64_t at = (((int64_t)max(page, 0) * a.hkv + h) << a.cache.page_shift) + (key & ((1 << a.cache.page_shift) - 1));
+            rs = make_rsrc_n(base + at * D, page < 0 ? 0 : have * kRow);
         } else {
             const int64_t at = k0 + min(key, max(keys - 1, 0));
             rs = make_rsrc_n(base + at * (is_k ? a.k_token : a.v_token) + (int64_t)h * (is_k ? a.k_head : a.v_head),
@@ -155,66 +185,44 @@ template <int D, bool F16, bool PAGED, int RT> __global__ __launch_bounds__(64 *
         v_rd[c] = 2 * kBuf + r * kRow + 16 * (u ^ v_swz<D>(r)) + 8 * (lane & 1);
     }
 
-    f32x16 o[RT][kTiles] = {}, x[RT][2];
-    float m[RT], l[RT];
-#pragma unroll
-    for (int r = 0; r < RT; ++r)
-        m[r] = kLowest, l[r] = 0.f;
+    f32x16 o[kTiles] = {}, x[2];
+    float m = kLowest, l = 0.f;
 
-    // element i of x[r][sub] is the score of key 64 t + 32 sub + 8 (i / 4) + 4 half + i % 4
-    auto scores = [&](int t, f32x16 (&y)[RT][2]) {
+    // element i of y[sub] is the score of key 64 t + 32 sub + 8 (i / 4) + 4 half + i % 4
+    auto scores = [&](int t, f32x16 (&y)[2]) {
         const uint8_t *const buf = lds + (t & 1) * kBuf;
-#pragma unroll
-        for (int r = 0; r < RT; ++r)
-            y[r][0] = f32x16{}, y[r][1] = f32x16{};
+        y[0] = f32x16{}, y[1] = f32x16{};
 #pragma unroll
         for (int s = 0; s < kSteps; ++s)
 #pragma unroll
-            for (int sub = 0; sub < 2; ++sub) {
-                const u32x4 k = *reinterpret_cast<const u32x4 *>(buf + k_rd[s] + 32 * kRow * sub);
-#pragma unroll
-                for (int r = 0; r < RT; ++r)
-                    y[r][sub] = mfma32x32x16<F16>(k, q[r][s], y[r][sub]);
-            }
+            for (int sub = 0; sub < 2; ++sub)
+                y[sub] = mfma32x32x16<F16>(*reinterpret_cast<const u32x4 *>(buf + k_rd[s] + 32 * kRow * sub), q[s], y[sub]);
     };
-    auto hide = [&](int t, f32x16 (&y)[RT][2]) {
+    auto hide = [&](int t, f32x16 (&y)[2]) {
+        const int left = seen - kKeys * t - 4 * half; // visible keys from this lane's first on
 #pragma unroll
-        for (int r = 0; r < RT; ++r) {
-            const int left = seen[r] - kKeys * t - 4 * half; // visible keys from this lane's first on
+        for (int i = 0; i < 32; ++i)
+            if (32 * (i >> 4) + 8 * ((i & 15) >> 2) + (i & 3) >= left)
+                y[i >> 4][i & 15] = -INFINITY;
+    };
+    auto highest = [&](const f32x16 (&y)[2]) {
+        float t0 = y[0][0], t1 = y[1][0];
 #pragma unroll
-            for (int i = 0; i < 32; ++i)
-                if (32 * (i >> 4) + 8 * ((i & 15) >> 2) + (i & 3) >= left)
-                    y[r][i >> 4][i & 15] = -INFINITY;
+        for (int i = 1; i < 15; i += 2) {
+            t0 = fmaxf(fmaxf(t0, y[0][i]), y[0][i + 1]);
+            t1 = fmaxf(fmaxf(t1, y[1][i]), y[1][i + 1]);
         }
+        t0 = fmaxf(fmaxf(t0, y[0][15]), t1);
+        return max_swap32(fmaxf(t0, y[1][15])) * a.scale_log2 - kHeadroom<F16>;
     };
-    auto highest = [&](const f32x16 (&y)[RT][2], float (&top)[RT]) {
+    auto raise = [&](float top) {
+        if (__builtin_amdgcn_ballot_w64(top > m + kRescaleSlack)) {
+            const float to = fmaxf(m, top), f = exp2_fast(m - to);
+            m = to;
+            l *= f;
 #pragma unroll
-        for (int r = 0; r < RT; ++r) {
-            float t0 = y[r][0][0], t1 = y[r][1][0];
-#pragma unroll
-            for (int i = 1; i < 15; i += 2) {
-                t0 = fmaxf(fmaxf(t0, y[r][0][i]), y[r][0][i + 1]);
-                t1 = fmaxf(fmaxf(t1, y[r][1][i]), y[r][1][i + 1]);
-            }
-            t0 = fmaxf(fmaxf(t0, y[r][0][15]), t1);
-            top[r] = max_swap32(fmaxf(t0, y[r][1][15])) * a.scale_log2 - kHeadroom<F16>;
-        }
-    };
-    auto raise = [&](const float (&top)[RT]) {
-        bool grows = false;
-#pragma unroll
-        for (int r = 0; r < RT; ++r)
-            grows |= top[r] > m[r] + kRescaleSlack;
-        if (__builtin_amdgcn_ballot_w64(grows)) {
-#pragma unroll
-            for (int r = 0; r < RT; ++r) {
-                const float to = fmaxf(m[r], top[r]), f = exp2_fast(m[r] - to);
-                m[r] = to;
-                l[r] *= f;
-#pragma unroll
-                for (int c = 0; c < kTiles; ++c)
-                    o[r][c] *= f;
-            }
+            for (int c = 0; c < kTiles; ++c)
+                o[c] *= f;
         }
     };
     // An infinity or NaN in V at a key that some rows do not see: 0 V would
@@ -235,9 +243,7 @@ template <int D, bool F16, bool PAGED, int RT> __global__ __launch_bounds__(64 *
                         for (int e = 0; e < 4; ++e) {
                             const uint32_t b = v[e >> 1] >> (16 * (e & 1)) & 0xFFFFu;
                             const bool odd = nonfinite_halves<F16>(b) != 0;
-#pragma unroll
-                            for (int r = 0; r < RT; ++r)
-                                o[r][c][4 * i + e] += odd && kKeys * t + key < seen[r] ? half_bits_to_f32<F16>(b) : 0.f;
+                            o[c][4 * i + e] += odd && kKeys * t + key < seen ? half_bits_to_f32<F16>(b) : 0.f;
                         }
                     }
                 }
@@ -259,26 +265,27 @@ template <int D, bool F16, bool PAGED, int RT> __global__ __launch_bounds__(64 *
     };
 
     // Tile t: p from its scores x, while the products of the next tile's
-    // scores run; then P V, while the next scores' maximum is taken.
+    // scores run; then P V, while the next scores' maximum is taken.  The sum
+    // is taken over the rounded p, so that their rounding cancels where a
+    // row's weight sits on few keys.
     auto step = [&](int t, auto more, auto masked) {
-        f32x16 y[RT][2];
-        u32x4 p[RT][4];
+        f32x16 y[2];
+        u32x4 p[4];
         if constexpr (more)
             scores(t + 1, y);
 #pragma unroll
-        for (int r = 0; r < RT; ++r)
-#pragma unroll
-            for (int i = 0; i < 32; i += 2) {
-                const uint32_t w = pack_half_x2<F16>(exp2_fast(x[r][i >> 4][i & 15] * a.scale_log2 - m[r]),
-                                                     exp2_fast(x[r][i >> 4][(i & 15) + 1] * a.scale_log2 - m[r]));
-                p[r][i >> 3][(i & 7) >> 1] = w;
-                l[r] = dot_ones<F16>(w, l[r]);
-            }
-        if constexpr (more && masked)
-            hide(t + 1, y);
-        float top[RT];
-        if constexpr (more)
-            highest(y, top);
+        for (int i = 0; i < 32; i += 2) {
+            const uint32_t w = pack_half_x2<F16>(exp2_fast(x[i >> 4][i & 15] * a.scale_log2 - m),
+                                                 exp2_fast(x[i >> 4][(i & 15) + 1] * a.scale_log2 - m));
+            p[i >> 3][(i & 7) >> 1] = w;
+            l = dot_ones<F16>(w, l);
+        }
+        float top = 0.f;
+        if constexpr (more) {
+            if constexpr (masked)
+                hide(t + 1, y);
+            top = highest(y);
+        }
         const uint8_t *const buf = lds + (t & 1) * kBuf;
 #pragma unroll
         for (int ks = 0; ks < 4; ++ks)
@@ -286,32 +293,28 @@ template <int D, bool F16, bool PAGED, int RT> __global__ __launch_bounds__(64 *
             for (int c = 0; c < kTiles; ++c) {
                 const u32x2 lo = lds_read_tr(buf + v_rd[c] + 16 * ks * kRow);
                 const u32x2 hi = lds_read_tr(buf + v_rd[c] + (16 * ks + 8) * kRow);
-                const u32x4 v = {lo[0], lo[1], hi[0], hi[1]};
-#pragma unroll
-                for (int r = 0; r < RT; ++r)
-                    o[r][c] = mfma32x32x16<F16>(v, p[r][ks], o[r][c]);
+                o[c] = mfma32x32x16<F16>(u32x4{lo[0], lo[1], hi[0], hi[1]}, p[ks], o[c]);
             }
         if constexpr (more) {
             raise(top);
-#pragma unroll
-            for (int r = 0; r < RT; ++r)
-                x[r][0] = y[r][0], x[r][1] = y[r][1];
+            x[0] = y[0], x[1] = y[1];
         }
     };
 
-    if (tiles > 0) {
-        fetch(true, 0, page_of(0));
-        fetch(false, 0, page_of(0));
-        fetch(true, 1, page_of(1));
-        int next_page = page_of(1), far_page = page_of(2);
+    if (tiles > t0) {
+        pages_from(t0);
+        fetch(true, t0, page_of(t0));
+        fetch(false, t0, page_of(t0));
+        if (((t0 + 1) & 63) == 0)
+            pages_from(t0 + 1);
+        int next_page = page_of(t0 + 1);
+        fetch(true, t0 + 1, next_page);
         wait_vmcnt<2 * kDmas>(); // the wave's copies of the first keys
         lds_barrier();
-        scores(0, x);
-        if (whole == 0)
-            hide(0, x);
-        float top[RT];
-        highest(x, top);
-        raise(top);
+        scores(t0, x);
+        if (t0 >= whole)
+            hide(t0, x);
+        raise(highest(x));
         // Before tile t: its values and the next tile's keys are there for
         // everybody, and the buffers of the values before and of its own keys
         // are used up.
@@ -332,19 +335,21 @@ template <int D, bool F16, bool PAGED, int RT> __global__ __launch_bounds__(64 *
                 wait_lgkmcnt0();
             }
             lds_barrier();
-            if (t + 2 < tiles)
-                fetch(true, t + 2, far_page);
             if (t + 1 < tiles)
                 fetch(false, t + 1, next_page);
-            next_page = far_page;
-            far_page = page_of(t + 3);
+            if (t + 2 < tiles) {
+                if (((t + 2) & 63) == 0)
+                    pages_from(t + 2);
+                next_page = page_of(t + 2);
+                fetch(true, t + 2, next_page);
+            }
             if constexpr (check) {
                 const uint32_t bad = s_bad[t & 1][0] | s_bad[t & 1][1] | s_bad[t & 1][2] | s_bad[t & 1][3];
                 if (__builtin_amdgcn_readfirstlane((int)bad))
                     mend(t);
             }
         };
-        int t = 0;
+        int t = t0;
         for (; t + 1 < whole && t + 1 < tiles; ++t) {
             turn(t, std::false_type{});
             step(t, std::true_type{}, std::false_type{});
@@ -357,35 +362,116 @@ template <int D, bool F16, bool PAGED, int RT> __global__ __launch_bounds__(64 *
         step(t, std::false_type{}, std::true_type{});
     }
 
+    const float sum = sum_swap32(l);
+    if (row >= rows)
+        return;
+    if (a.splits > 1) {
+        const int64_t at = row_out * a.splits + split;
 #pragma unroll
-    for (int r = 0; r < RT; ++r) {
-        const float sum = sum_swap32(l[r]);
-        const float inv = sum == 0.f ? 1.f : 1.f / sum;
-        if (row[r] < rows) {
+        for (int c = 0; c < kTiles; ++c)
 #pragma unroll
-            for (int c = 0; c < kTiles; ++c)
-#pragma unroll
-                for (int i = 0; i < 16; i += 4) {
-                    const u32x2 w = {pack_half_x2<F16>(o[r][c][i] * inv, o[r][c][i + 1] * inv),
-                                     pack_half_x2<F16>(o[r][c][i + 2] * inv, o[r][c][i + 3] * inv)};
-                    *reinterpret_cast<u32x2 *>(a.out + at_out[r] + 32 * c + 2 * i) = w;
-                }
+            for (int i = 0; i < 16; i += 4)
+                *reinterpret_cast<f32x4 *>(a.part + at * D + 32 * c + 2 * i + 4 * half) =
+                    f32x4{o[c][i], o[c][i + 1], o[c][i + 2], o[c][i + 3]};
+        if (half == 0) {
+            a.stats[2 * at] = m;
+            a.stats[2 * at + 1] = sum;
         }
+        return;
+    }
+    const float inv = sum == 0.f ? 1.f : 1.f / sum;
+    uint16_t *const p = a.out + row_out * D + 4 * half;
+#pragma unroll
+    for (int c = 0; c < kTiles; ++c)
+#pragma unroll
+        for (int i = 0; i < 16; i += 4)
+            *reinterpret_cast<u32x2 *>(p + 32 * c + 2 * i) = u32x2{pack_half_x2<F16>(o[c][i] * inv, o[c][i + 1] * inv),
+                                                                   pack_half_x2<F16>(o[c][i + 2] * inv, o[c][i + 3] * inv)};
+}
+
+// Few rows and many keys: the ranges of a row's keys joined,
+// o = sum_i 2^(m_i - m) O_i / sum_i 2^(m_i - m) l_i, a lane for 4 channels.
+// Bound by the latency of reading a row's partial results.
+template <int D, bool F16, bool PAGED> __global__ __launch_bounds__(256) void attn_prefill_join_kernel(PrefillArgs a)
+{
+    constexpr int kLanes = D / 4, kRows = 256 / kLanes;
+    const int h = blockIdx.x % a.hkv, seq = blockIdx.x / a.hkv;
+    const int q0 = clampi(a.cu_q[seq], 0, a.tokens);
+    const int all_new = max(clampi(a.cu_q[seq + 1], 0, a.tokens) - q0, 0);
+    const int64_t rows = (int64_t)min(all_new, a.longest) * a.G;
+    int keys;
+    if constexpr (PAGED) {
+        keys = clampi(a.lens[seq], 0, a.cache.width << a.cache.page_shift);
+    } else {
+        const int k0 = clampi(a.cu_k[seq], 0, a.keys);
+        keys = max(clampi(a.cu_k[seq + 1], 0, a.keys) - k0, 0);
+    }
+    const int shift = keys - all_new + 1, per = prefill_range(keys, a.splits);
+    const int c = 4 * (threadIdx.x % kLanes);
+    for (int64_t row = (int64_t)blockIdx.y * kRows + threadIdx.x / kLanes; row < rows; row += (int64_t)gridDim.y * kRows) {
+        const int64_t last = min(rows, row / kPrefillRows * kPrefillRows + kPrefillRows) - 1; // of the row's block
+        const int tiles = (clampi(shift + (int)(last / a.G), 0, keys) + kKeys - 1) / kKeys;
+        const int n = max(1, (tiles + per - 1) / per);
+        const int64_t at = (q0 + row / a.G) * a.hkv * a.G + h * a.G + row % a.G;
+        const float *const st = a.stats + 2 * at * a.splits;
+        const float *const part = a.part + at * a.splits * D + c;
+        float top = st[0];
+        for (int i = 1; i < n; ++i)
+            top = fmaxf(top, st[2 * i]);
+        f32x4 x = {};
+        float sum = 0.f;
+        for (int i = 0; i < n; ++i) {
+            const float f = exp2_fast(st[2 * i] - top);
+            sum += f * st[2 * i + 1];
+            x += f * *reinterpret_cast<const f32x4 *>(part + (int64_t)i * D);
+        }
+        const float inv = sum == 0.f ? 1.f : 1.f / sum;
+        *reinterpret_cast<u32x2 *>(a.out + at * D + c) = u32x2{pack_half_x2<F16>(x[0] * inv, x[1] * inv),
+                                                               pack_half_x2<F16>(x[2] * inv, x[3] * inv)};
     }
 }
 
 template <int D, bool F16, bool PAGED> hipError_t run(const PrefillArgs &a, int64_t seqs, hipStream_t st)
 {
-    constexpr int RT = PF_RT;
-    const int64_t tiles = ((int64_t)a.longest * a.G + 128 * RT - 1) / (128 * RT);
-    attn_prefill_kernel<D, F16, PAGED, RT><<<dim3((unsigned)(a.hkv * seqs), (unsigned)tiles), 64 * kWaves, 8 * kKeys * D, st>>>(a);
+    const int64_t bundles = (seqs + a.seqs_by - 1) / a.seqs_by * (a.hkv / a.heads_by);
+    const dim3 grid((unsigned)(bundles * a.seqs_by * a.heads_by * a.blocks), (unsigned)a.splits);
+    attn_prefill_kernel<D, F16, PAGED><<<grid, 64 * kWaves, 8 * kKeys * D, st>>>(a);
+    if (hipError_t e = hipGetLastError(); e != hipSuccess || a.splits == 1)
+        return e;
+    const int64_t rows = (int64_t)a.longest * a.G, each = 1024 / D;
+    attn_prefill_join_kernel<D, F16, PAGED>
+        <<<dim3((unsigned)(a.hkv * seqs), (unsigned)std::min<int64_t>((rows + each - 1) / each, 32768)), 256, 0, st>>>(a);
     return hipGetLastError();
 }
 
 } // namespace
 
-hipError_t launch_attn_prefill(const PrefillArgs &a, int D, bool f16, bool paged, int64_t seqs, hipStream_t st)
+// Few row blocks: the keys of a sequence are cut into ranges, so that the
+// device is filled once (two workgroups a compute unit), and joined.  A range
+// is at least kMinRange tiles: PLACE.
+int plan_prefill_splits(int64_t seqs, int64_t T, int64_t hkv, int64_t G, int64_t longest, int64_t keys, int cus)
 {
+    const int64_t blocks = hkv * std::min(seqs * prefill_blocks(longest, G), T * G / kPrefillRows + seqs);
+    const int64_t ranges = (keys + kKeys * kMinRange - 1) / (kKeys * kMinRange);
+    const int64_t splits = std::min<int64_t>({2 * (int64_t)cus / std::max<int64_t>(1, blocks), ranges, kMaxSplits});
+    return ranges > 2 ? (int)std::max<int64_t>(1, splits) : 1;
+}
+
+hipError_t launch_attn_prefill(PrefillArgs a, int D, bool f16, bool paged, int64_t seqs, hipStream_t st)
+{
+    a.blocks = (int)prefill_blocks(a.longest, a.G);
+    // How many (sequence, key-value head) pairs run side by side: as many as
+    // leave their keys and values in an XCD's L2 (a sequence taken to have
+    // the mean number of keys, or for pages what its table can name), at
+    // least eight heads or one sequence's.
+    const int64_t keys = paged ? (int64_t)a.cache.width << a.cache.page_shift : a.keys / seqs;
+    const int64_t pairs = 8 * std::max<int64_t>(1, kL2Share / std::max<int64_t>(1, keys * 4 * D));
+    a.heads_by = (int)std::min<int64_t>(a.hkv, pairs);
+    while (a.hkv % a.heads_by)
+        --a.heads_by;
+    const int64_t by = a.heads_by == a.hkv ? std::max<int64_t>(1, std::min<int64_t>(pairs / a.hkv, seqs)) : 1;
+    const int64_t bundles = (seqs + by - 1) / by;
+    a.seqs_by = (int)((seqs + bundles - 1) / bundles);
     if (D == 64)
         return paged ? f16 ? run<64, true, true>(a, seqs, st) : run<64, false, true>(a, seqs, st)
                : f16 ? run<64, true, false>(a, seqs, st)

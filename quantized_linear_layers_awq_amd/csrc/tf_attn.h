@@ -39,8 +39,16 @@ struct PrefillArgs {
     uint16_t *out;                     // [T][Hq][D]
     int tokens, keys, hkv, G, longest;
     float scale_log2;
+    int seqs, splits; // ranges of keys
+    float *part;      // [T][Hq][splits][D], when splits > 1
+    float *stats;     // [T][Hq][splits][2]: maximum, sum
+    // set by the launch: row blocks of a (sequence, head), and how many heads and sequences stand next to each other in the grid
+    int blocks, heads_by, seqs_by;
 };
-hipError_t launch_attn_prefill(const PrefillArgs &a, int D, bool f16, bool paged, int64_t seqs, hipStream_t st);
+constexpr int kPrefillRows = 128; // rows (token, head of a group) of a workgroup
+inline int64_t prefill_blocks(int64_t longest, int64_t G) { return (longest * G + kPrefillRows - 1) / kPrefillRows; }
+int plan_prefill_splits(int64_t seqs, int64_t T, int64_t hkv, int64_t G, int64_t longest, int64_t keys, int cus);
+hipError_t launch_attn_prefill(PrefillArgs a, int D, bool f16, bool paged, int64_t seqs, hipStream_t st);
 
 // ---- the cache -----------------------------------------------------------------
 struct AppendArgs {

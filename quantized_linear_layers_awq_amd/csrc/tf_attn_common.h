@@ -57,13 +57,24 @@ __device__ __forceinline__ float sum_swap32(float x)
 // a 4 x 16 matrix, and lane j receives its column j (rows 0..3).
 typedef short s16x2 __attribute__((ext_vector_type(2)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
-__device__ __forceinline__ u32x2 lds_read_tr(const uint8_t *p)
+__device__ __forceinline__ u32x2 lds_read_tr(const uint8_t *__restrict__ p)
 {
     return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
                                          (__attribute__((address_space(3))) s16x4 *)p));
 }
 
 __device__ __forceinline__ int clampi(int v, int lo, int hi) { return v < lo ? lo : v > hi ? hi : v; }
+
+// Rows of a run of 16 that lie before `end`; all arguments uniform.  The empty
+// asm keeps the compiler from joining the two bounds to a clamp, which it puts
+// on the vector unit even for uniform values: a buffer resource made from it
+// is then looped over lane by lane.
+__device__ __forceinline__ int rows_before(int end, int first)
+{
+    int left = max(end - first, 0);
+    asm("" : "+s"(left));
+    return min(left, 16);
+}
 
 // A raw buffer of `bytes` bytes: lanes at or past the end read zeros without
 // a memory access.

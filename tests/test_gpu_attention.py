@@ -384,3 +384,59 @@ def test_fp16_keeps_the_small_weights_of_a_long_row():
         # a weight is rounded to half of fp16's smallest step, 2^-25, against a maximum held at 2^7; the sum, one rounding
         tol = n * 2.0**-32 + 3 * 2.0**-11 * want
         assert bool(((out.double() - want).abs() <= tol).all()), (out.flatten()[:2].tolist(), want)
+
+
+@pytest.mark.parametrize("t", ["bf16", "f16"])
+@pytest.mark.parametrize("new,nkeys,heads,page", [
+    # few rows behind many keys: the keys are cut into ranges and joined
+    ([1], [5000], (8, 1, 128), 16), ([37, 0, 5], [3001, 0, 700], (28, 4, 128), 64), ([130], [4097], (14, 2, 64), 16),
+    ([400, 3], [1500, 4500], (8, 1, 128), 128), ([7, 9, 40], [7, 2, 2000], (71, 1, 64), 32), ([900], [900], (4, 2, 64), 16),
+])
+@pytest.mark.parametrize("paged", [False, True])
+def test_prefill_ranges_of_keys(new, nkeys, heads, page, paged, t):
+    _, q_ = gpu_or_skip()
+    hq, hkv, d = heads
+    print(f"prefill ranges {t} paged={paged} {heads} page {page} new {new} keys {nkeys}", flush=True)
+    g = _gen(sum(new) + 3 * sum(nkeys) + hq)
+    cu, ck = _starts(new), _starts(nkeys)
+    cu_q = torch.tensor(cu, dtype=torch.int32, device=DEV)
+    q = _normal(g, (sum(new), hq, d), TYPES[t], 1.5)
+    if paged:
+        tables, pages = ref.tables_for(nkeys, page, g)
+        kp, vp = (_normal(g, (pages, hkv, page, d), TYPES[t]) for _ in "kv")
+        assert q_.tf_attn_prefill_workspace_bytes(len(new), sum(new), hq, hkv, d, max(new), tables.shape[1] * page) > 0
+        out = q_.tf_attn_prefill_paged(q, kp, vp, tables.to(DEV), cu_q, torch.tensor(nkeys, dtype=torch.int32, device=DEV), max(new))
+
+        def keys_of(s, h):
+            return ref.gather(kp, tables[s], nkeys[s], h), ref.gather(vp, tables[s], nkeys[s], h)
+    else:
+        k, v = (_normal(g, (sum(nkeys), hkv, d), TYPES[t]) for _ in "kv")
+        need = q_.tf_attn_prefill_workspace_bytes(len(new), sum(new), hq, hkv, d, max(new), sum(nkeys))
+        assert need > 0
+        ws = torch.full((need // 4,), float("nan"), device=DEV)  # what it holds does not matter
+        out = q_.tf_attn_prefill(q, k, v, cu_q, torch.tensor(ck, dtype=torch.int32, device=DEV), max(new), workspace=ws)
+        small = ws[:-1]
+        with pytest.raises(q_.TileFuseError, match="(?i)buffer|workspace|small"):
+            q_.tf_attn_prefill(q, k, v, cu_q, torch.tensor(ck, dtype=torch.int32, device=DEV), max(new), workspace=small)
+
+        def keys_of(s, h):
+            return k[ck[s]:ck[s + 1], h].double(), v[ck[s]:ck[s + 1], h].double()
+    torch.cuda.synchronize()
+    _check_prefill(q, keys_of, cu, nkeys, hkv, d ** -0.5, out)
+
+
+def test_prefill_infinities_past_a_range():
+    """Infinities and NaN in values of every range, seen by some rows and not by others."""
+    _, q_ = gpu_or_skip()
+    n, new, hq, hkv, d = 2500, 60, 6, 2, 128
+    g = _gen(31)
+    q = _normal(g, (new, hq, d), torch.float16)
+    k, v = (_normal(g, (n, hkv, d), torch.float16) for _ in "kv")
+    for at, h, c, x in ((2490, 0, 3, "inf"), (2470, 1, 90, "-inf"), (2445, 1, 5, "nan"), (2499, 0, 127, "nan"), (2450, 0, 64, "inf")):
+        v[at, h, c] = float(x)
+    print("infinities past a range", flush=True)
+    ints = [torch.tensor([0, x], dtype=torch.int32, device=DEV) for x in (new, n)]
+    assert q_.tf_attn_prefill_workspace_bytes(1, new, hq, hkv, d, new, n) > 0
+    out = q_.tf_attn_prefill(q, k, v, *ints, new, 0.2)
+    torch.cuda.synchronize()
+    _check_prefill(q, lambda s, h: (k[:, h].double(), v[:, h].double()), [0, new], [n], hkv, 0.2, out)

@@ -79,12 +79,11 @@ template <int D, bool F16, bool PAGED> __global__ __launch_bounds__(64 * kWaves,
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int half = lane >> 5, n = lane & 31;
     // bundle of sequences, group of heads, block of rows, sequence in the
-    // bundle, head in the group (fastest).  The sequences turn with the block,
-    // so that no XCD is left with the same ones throughout.
+    // bundle, head in the group (fastest)
     const int pairs = a.seqs_by * a.heads_by, groups = a.hkv / a.heads_by;
     const int bundle = blockIdx.x / (a.blocks * pairs), rest = blockIdx.x % (a.blocks * pairs);
     const int block = a.blocks - 1 - rest / pairs, pair = rest % pairs;
-    const int seq = bundle / groups * a.seqs_by + (pair / a.heads_by + block % a.seqs_by) % a.seqs_by;
+    const int seq = bundle / groups * a.seqs_by + pair / a.heads_by;
     const int h = bundle % groups * a.heads_by + pair % a.heads_by;
     if (seq >= a.seqs)
         return;
@@ -463,13 +462,17 @@ hipError_t launch_attn_prefill(PrefillArgs a, int D, bool f16, bool paged, int64
     // How many (sequence, key-value head) pairs run side by side: as many as
     // leave their keys and values in an XCD's L2 (a sequence taken to have
     // the mean number of keys, or for pages what its table can name), at
-    // least eight heads or one sequence's.
+    // least eight heads or one sequence's.  Sequences run side by side only
+    // where the heads' number keeps each head on one XCD: otherwise the
+    // XCDs would share out the sequences, long and short ones (two sequences
+    // of 4096 and fewer tokens, 14/2 heads of 64: 78 us, and 60 in turn).
     const int64_t keys = paged ? (int64_t)a.cache.width << a.cache.page_shift : a.keys / seqs;
     const int64_t pairs = 8 * std::max<int64_t>(1, kL2Share / std::max<int64_t>(1, keys * 4 * D));
     a.heads_by = (int)std::min<int64_t>(a.hkv, pairs);
     while (a.hkv % a.heads_by)
         --a.heads_by;
-    const int64_t by = a.heads_by == a.hkv ? std::max<int64_t>(1, std::min<int64_t>(pairs / a.hkv, seqs)) : 1;
+    const bool side = a.heads_by == a.hkv && a.hkv % 8 == 0;
+    const int64_t by = side ? std::max<int64_t>(1, std::min<int64_t>(pairs / a.hkv, seqs)) : 1;
     const int64_t bundles = (seqs + by - 1) / by;
     a.seqs_by = (int)((seqs + bundles - 1) / bundles);
     if (D == 64)

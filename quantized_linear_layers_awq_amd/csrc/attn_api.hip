@@ -70,9 +70,12 @@ bool scale_ok(float s) { return std::isfinite(s) && s > 0.f; }
 
 constexpr float kLog2E = 1.4426950408889634f;
 
-int64_t decode_part_floats(int64_t seqs, int64_t Hq, int64_t D, const tf::DecodePlan &p)
+// Rows of a decode call's partial results, and its workspace: the rows, their
+// maxima and sums, three numbers per share.
+int64_t decode_part_rows(const tf::DecodePlan &p) { return p.shares * 2 * 16 * p.nt; }
+size_t decode_ws(int64_t D, const tf::DecodePlan &p)
 {
-    return p.splits > 1 ? seqs * Hq * p.splits * (D + 2) : 0;
+    return (size_t)(decode_part_rows(p) * (D + 2) + 3 * p.shares) * sizeof(float);
 }
 
 int check_decode_sizes(int type, int64_t seqs, int64_t Hq, int64_t Hkv, int64_t D, int64_t longest)
@@ -207,7 +210,7 @@ size_t tf_attn_decode_workspace_bytes(int64_t seqs, int64_t Hq, int64_t Hkv, int
     if (check_decode_sizes(TF_TYPE_BF16, seqs, Hq, Hkv, D, longest) != TF_OK || seqs == 0)
         return 0;
     const tf::DecodePlan p = tf::plan_decode(seqs, Hkv, Hq / Hkv, longest, tf::device_cus());
-    return (size_t)decode_part_floats(seqs, Hq, D, p) * sizeof(float);
+    return decode_ws(D, p);
 }
 
 int tf_attn_decode(int type, const uint16_t *q, int64_t q_token, int64_t q_head, const uint16_t *k_pages,
@@ -230,10 +233,9 @@ int tf_attn_decode(int type, const uint16_t *q, int64_t q_token, int64_t q_head,
     if (int st = check_paged(k_pages, v_pages, pages, page, tables, width))
         return st;
     const tf::DecodePlan p = tf::plan_decode(seqs, Hkv, Hq / Hkv, longest, tf::device_cus());
-    const int64_t floats = decode_part_floats(seqs, Hq, D, p);
-    if (int st = check_ws(workspace, ws_bytes, (size_t)floats * sizeof(float)))
+    if (int st = check_ws(workspace, ws_bytes, decode_ws(D, p)))
         return st;
-    tf::DecodeArgs a;
+    tf::DecodeArgs a = {};
     a.q = q;
     a.q_token = q_token;
     a.q_head = q_head;
@@ -241,13 +243,16 @@ int tf_attn_decode(int type, const uint16_t *q, int64_t q_token, int64_t q_head,
     a.lens = lens;
     a.out = out;
     a.part = static_cast<float *>(workspace);
-    a.stats = floats ? a.part + seqs * Hq * p.splits * D : nullptr;
+    if (p.shares) {
+        a.stats = a.part + decode_part_rows(p) * D;
+        a.spans = reinterpret_cast<int32_t *>(a.stats + 2 * decode_part_rows(p));
+    }
+    a.seqs = (int)seqs;
     a.G = (int)(Hq / Hkv);
+    a.groups = (int)p.groups;
     a.longest = (int)std::min<int64_t>(longest, width * page);
-    a.chunk = (int)p.chunk;
-    a.splits = (int)p.splits;
     a.scale_log2 = scale * kLog2E;
-    return tf::launch_attn_decode(a, (int)D, type == TF_TYPE_F16, seqs, p, static_cast<hipStream_t>(stream)) == hipSuccess
+    return tf::launch_attn_decode(a, (int)D, type == TF_TYPE_F16, p, static_cast<hipStream_t>(stream)) == hipSuccess
                ? TF_OK
                : TF_ERR_HIP;
 }

@@ -7,19 +7,23 @@
 // What bounds it: the cache is read once, 4 D bytes per token and key-value
 // head against 4 G D operations, so HBM does.  The kernel is a stream of
 // key tiles with the arithmetic hidden under it:
-//  - One workgroup of 8 waves per (chunk of keys, key-value head, sequence,
-//    group of 16 NT query heads).  Each wave takes every eighth 32-key tile
-//    of the chunk on its own: K goes from memory straight into MFMA operand
-//    registers, V through the wave's own LDS buffer (row-major in, transposed
-//    out), the next tile's loads in flight meanwhile.  No barrier before the
-//    end.
+//  - A workgroup's 8 waves each take every eighth 32-key tile of its range on
+//    their own: K goes from memory straight into MFMA operand registers, V
+//    through the wave's own LDS buffer (row-major in, transposed out), the
+//    next tile's loads in flight meanwhile.  No barrier before the end.
 //  - Both products run on 16x16x32 MFMAs with the query heads as columns, so
 //    the heads of a group share one read of the cache.
 //  - Page ids of 32 tiles are fetched by one load per wave (a lane per
 //    16-key run) and read out lane by lane, off the critical path.
-//  - The waves' (m, l, O) are joined in LDS in wave order.  With one chunk
-//    the workgroup writes the output; otherwise it writes fp32 partials and
-//    attn_join_kernel adds the chunks in order.  No atomics.
+//  - The waves' (m, l, O) are joined in LDS in wave order.
+//  - Short caches: a workgroup per (sequence, key-value head, group of 16 NT
+//    query heads), which writes the output.  Long ones: the keys of all
+//    (sequence, head, group) items, counted in rounds of 8 tiles, are laid end
+//    to end and cut into equal shares, one per workgroup and compute unit,
+//    so that ragged lengths leave no tail.  A workgroup
+//    finds its share from a prefix sum of the lengths.  Items that lie whole
+//    in a share are written; the others' fp32 partials are added by
+//    attn_join_kernel in order.  No atomics.
 #include "tf_attn.h"
 
 namespace tf {
@@ -28,6 +32,12 @@ namespace {
 
 constexpr int kWaves = 8;
 constexpr int kTile = 32;
+// Cache policy of the keys and values: streamed (nt), for they are read once a
+// step and the next layer's displace them.  Against the default, four caches
+// in turn: 16 contexts of up to 32768 tokens (1.12 GB) 174 us and 193, one of
+// 131072 89 and 99; where one cache of 240 MB is read again and again and
+// stays in the last-level cache, 48 and 44.
+constexpr int kStream = 2;
 
 template <int D> struct Stage {
     u32x4 k[2][D / 32]; // sub-tile of 16 keys, 32-channel step
@@ -36,7 +46,64 @@ template <int D> struct Stage {
 
 template <int D> constexpr int v_swz(int row) { return D == 128 ? 2 * (row & 7) : 2 * ((row >> 1) & 3); }
 
-template <int D, bool F16, int NT> __global__ __launch_bounds__(64 * kWaves, 2) void attn_decode_kernel(DecodeArgs a)
+// The position of a workgroup's share: the sequence it begins in, and the
+// rounds of the sequences before that one.
+struct Start {
+    int64_t rounds; // of all sequences, one item each
+    int64_t before;
+    int seq;
+};
+
+__device__ __forceinline__ int rounds_of(int len, int round) { return (len + round - 1) / round; }
+
+// Finds rounds, and the sequence of the unit-th round of an item (unit(rounds)
+// names it; past the end: seq = seqs).  Every thread takes a strip of sequences.
+template <int THREADS, typename Unit> __device__ __forceinline__ Start find_start(const DecodeArgs &a, int round, Unit unit)
+{
+    __shared__ int64_t s_sum[THREADS / 64];
+    __shared__ int64_t s_before;
+    __shared__ int s_seq;
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int strip = (a.seqs + THREADS - 1) / THREADS;
+    const int first = min(tid * strip, a.seqs), end = min(first + strip, a.seqs);
+    int64_t sum = 0;
+    for (int s = first; s < end; ++s)
+        sum += rounds_of(clampi(a.lens[s], 0, a.longest), round);
+    int64_t in = sum;
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) {
+        const int64_t y = __shfl_up(in, d);
+        in += lane >= d ? y : 0;
+    }
+    if (lane == 63)
+        s_sum[wave] = in;
+    if (tid == 0)
+        s_seq = a.seqs;
+    __syncthreads();
+    int64_t before = in - sum, all = 0;
+#pragma unroll
+    for (int w = 0; w < THREADS / 64; ++w) {
+        before += w < wave ? s_sum[w] : 0;
+        all += s_sum[w];
+    }
+    const int64_t at = unit(all);
+    if (before <= at && at < before + sum) {
+        int s = first;
+        for (;; ++s) {
+            const int r = rounds_of(clampi(a.lens[s], 0, a.longest), round);
+            if (at < before + r)
+                break;
+            before += r;
+        }
+        s_seq = s;
+        s_before = before;
+    }
+    __syncthreads();
+    return {all, s_before, __builtin_amdgcn_readfirstlane(s_seq)};
+}
+
+// SHARES: equal shares of all keys, else one item of one sequence
+template <int D, bool F16, int NT, bool SHARES> __global__ __launch_bounds__(64 * kWaves, 2) void attn_decode_kernel(DecodeArgs a)
 {
     constexpr int kSteps = D / 32;   // MFMA steps over channels
     constexpr int kTiles = D / 16;   // 16-channel tiles of O^T
@@ -44,19 +111,32 @@ template <int D, bool F16, int NT> __global__ __launch_bounds__(64 * kWaves, 2) 
     constexpr int kChunks = D / 8;   // 16-byte units of a row
     constexpr int kRowsPerLoad = 1024 / kRow;
     constexpr int kWaveBytes = kTile * kRow; // V of a tile; in the join, 16 heads of D floats
+    constexpr int kRound = kWaves * kTile;
     static_assert(kWaveBytes == 16 * D * 4, "the join reuses the V buffers");
     __shared__ __attribute__((aligned(16))) uint8_t lds[kWaves * kWaveBytes];
     __shared__ float s_m[kWaves][16], s_l[kWaves][16];
 
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int g = lane >> 4, n = lane & 15;
-    const int h = blockIdx.x % a.cache.hkv, group = blockIdx.x / a.cache.hkv;
-    const int seq = blockIdx.y, split = blockIdx.z;
-    const int len = clampi(a.lens[seq], 0, a.longest);
-    const int c0 = split * a.chunk, c1 = min(len, c0 + a.chunk);
-    if (c1 <= c0 && a.splits > 1)
-        return; // the join reads only the chunks that a sequence has
-    const int tiles = c1 > c0 ? (c1 - c0 + kTile - 1) / kTile : 0;
+    const int items = a.cache.hkv * a.groups; // of a sequence
+    uint8_t *const vbuf = lds + wave * kWaveBytes;
+
+    // V in LDS: unit c of row r at r kRow + 16 (c ^ v_swz(r))
+    const int wr_row = lane / kChunks, wr_unit = lane % kChunks;
+    uint32_t tr[kTiles];
+#pragma unroll
+    for (int t = 0; t < kTiles; ++t) {
+        const int r = 4 * g + (n >> 2), c = 2 * t + ((n >> 1) & 1);
+        tr[t] = r * kRow + 16 * (c ^ v_swz<D>(r)) + 8 * (n & 1);
+    }
+    const u32x4 ones = F16 ? u32x4{0x3C003C00u, 0x3C003C00u, 0x3C003C00u, 0x3C003C00u}
+                           : u32x4{0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u};
+
+    // Keys c0 .. c1 - 1 of an item; the result goes to the output (slot < 0)
+    // or to a slot of the partial results.
+    auto attend = [&](int seq, int item, int c0, int c1, int slot) {
+    const int h = item % a.cache.hkv, group = item / a.cache.hkv;
+    const int tiles = (c1 - c0 + kTile - 1) / kTile;
     const int row0 = group * 16 * NT; // first query head of the group here
 
     // Q^T operands: column n is head row0 + 16 nt + n
@@ -73,15 +153,14 @@ template <int D, bool F16, int NT> __global__ __launch_bounds__(64 * kWaves, 2) 
     const int32_t *table = a.cache.tables + (int64_t)seq * a.cache.width;
     const int page_mask = (1 << a.cache.page_shift) - 1;
     const int64_t page_elems = (int64_t)D << a.cache.page_shift;
-    uint8_t *const vbuf = lds + wave * kWaveBytes;
 
     // lane L: the page of 16-key run L % 2 of this wave's tile it0 + L / 2
     auto page_ids = [&](int it0) {
         const int key = c0 + kTile * (wave + kWaves * (it0 + (lane >> 1))) + 16 * (lane & 1);
         int id = -1;
-        if (key < c1)
+        if (key < a.longest) // not c1: the length may still be on its way
             id = table[key >> a.cache.page_shift];
-        return id >= 0 && id < a.cache.pages ? id : -1;
+        return key < c1 && id < a.cache.pages ? id : -1;
     };
     const uint32_t k_off = n * kRow + 16 * g, v_off = 16 * lane;
     auto load = [&](Stage<D> &st, int it, int ids) {
@@ -95,10 +174,10 @@ template <int D, bool F16, int NT> __global__ __launch_bounds__(64 * kWaves, 2) 
             const Rsrc kr = make_rsrc_n(a.cache.k + at, rows * kRow), vr = make_rsrc_n(a.cache.v + at, rows * kRow);
 #pragma unroll
             for (int s = 0; s < kSteps; ++s)
-                st.k[sub][s] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(kr, k_off + 64 * s, 0, 0));
+                st.k[sub][s] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(kr, k_off + 64 * s, 0, kStream));
 #pragma unroll
             for (int s = 0; s < kSteps; ++s)
-                st.v[sub][s] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(vr, v_off + 1024 * s, 0, 0));
+                st.v[sub][s] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(vr, v_off + 1024 * s, 0, kStream));
         }
     };
 
@@ -107,17 +186,6 @@ template <int D, bool F16, int NT> __global__ __launch_bounds__(64 * kWaves, 2) 
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
         m[nt] = kLowest;
-    // V in LDS: unit c of row r at r kRow + 16 (c ^ v_swz(r))
-    const int wr_row = lane / kChunks, wr_unit = lane % kChunks;
-    uint32_t tr[kTiles];
-#pragma unroll
-    for (int t = 0; t < kTiles; ++t) {
-        const int r = 4 * g + (n >> 2), c = 2 * t + ((n >> 1) & 1);
-        tr[t] = r * kRow + 16 * (c ^ v_swz<D>(r)) + 8 * (n & 1);
-    }
-    const u32x4 ones = F16 ? u32x4{0x3C003C00u, 0x3C003C00u, 0x3C003C00u, 0x3C003C00u}
-                           : u32x4{0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u};
-
     auto compute = [&](const Stage<D> &st, int it) {
 #pragma unroll
         for (int sub = 0; sub < 2; ++sub)
@@ -238,116 +306,167 @@ template <int D, bool F16, int NT> __global__ __launch_bounds__(64 * kWaves, 2) 
                 x += f * p[0];
                 y += f * p[1];
             }
-            const int64_t at = (int64_t)seq * a.cache.hkv * a.G + h * a.G + row0 + 16 * nt + r;
-            if (a.splits == 1) {
+            if (slot < 0) {
+                const int64_t at = (int64_t)seq * a.cache.hkv * a.G + h * a.G + row0 + 16 * nt + r;
                 const float inv = sum == 0.f ? 1.f : 1.f / sum;
                 *reinterpret_cast<uint32_t *>(a.out + at * D + c) = pack_half_x2<F16>(x * inv, y * inv);
             } else {
-                float *const part = a.part + (at * a.splits + split) * D + c;
-                part[0] = x;
-                part[1] = y;
-                if (c == 0) {
-                    a.stats[2 * (at * a.splits + split)] = top;
-                    a.stats[2 * (at * a.splits + split) + 1] = sum;
+                const int64_t at = (int64_t)slot * 16 * NT + 16 * nt + r;
+                *reinterpret_cast<f32x2 *>(a.part + at * D + c) = f32x2{x, y};
+                if (c == 0)
+                    *reinterpret_cast<f32x2 *>(a.stats + 2 * at) = f32x2{top, sum};
+            }
+        }
+    }
+    };
+
+    if constexpr (!SHARES) {
+        const int seq = blockIdx.y, len = clampi(a.lens[seq], 0, a.longest);
+        attend(seq, blockIdx.x, 0, __builtin_amdgcn_readfirstlane(len), -1);
+    } else {
+        const int me = blockIdx.x;
+        // sequences without keys have no rounds: their rows are zeroed here
+        for (int s = me; s < a.seqs; s += gridDim.x)
+            if (a.lens[s] <= 0 || a.longest == 0)
+                for (int64_t u = threadIdx.x; u < (int64_t)a.cache.hkv * a.G * (D / 8); u += 64 * kWaves)
+                    reinterpret_cast<u32x4 *>(a.out)[(int64_t)s * a.cache.hkv * a.G * (D / 8) + u] = u32x4{};
+        int64_t per = 0;
+        const Start from = find_start<64 * kWaves>(a, kRound, [&](int64_t all) {
+            per = (all * items + gridDim.x - 1) / gridDim.x;
+            return me * per / items;
+        });
+        const int64_t end = min(from.rounds * items, (me + 1) * per); // in rounds of items
+        int64_t at = me * per, before = from.before;
+        int seq = from.seq, spans = 0, first_item = 0, first_seq = 0;
+        while (at < end && seq < a.seqs) {
+            const int len = __builtin_amdgcn_readfirstlane(clampi(a.lens[seq], 0, a.longest));
+            const int r = rounds_of(len, kRound);
+            if (r > 0) {
+                const int64_t in = at - before * items;
+                const int item = __builtin_amdgcn_readfirstlane((int)(in / r));
+                const int off = __builtin_amdgcn_readfirstlane((int)(in - (int64_t)item * r));
+                const int take = __builtin_amdgcn_readfirstlane((int)min((int64_t)(r - off), end - at));
+                const bool begins = off == 0, ends = off + take == r;
+                attend(seq, item, off * kRound, min(len, (off + take) * kRound), begins && ends ? -1 : 2 * me + begins);
+                if (begins && !ends) { // this share and those up to the item's last round
+                    spans = (int)((at + r - 1) / per) - me + 1;
+                    first_seq = seq;
+                    first_item = item;
+                }
+                at += take;
+                if (item + 1 < items || !ends) {
+                    __syncthreads(); // the join has read the V buffers
+                    continue;
                 }
             }
+            before += r;
+            ++seq;
+            __syncthreads();
+        }
+        if (threadIdx.x == 0) {
+            a.spans[3 * me] = spans;
+            a.spans[3 * me + 1] = first_seq;
+            a.spans[3 * me + 2] = first_item;
         }
     }
 }
 
-// One query row per workgroup: o = sum_i 2^(m_i - m) O_i / sum_i 2^(m_i - m) l_i
-// over the row's chunks.  The four waves take every fourth chunk each and are
-// added in wave order; a handful of kilobytes per row, bound by latency.
-template <int D, bool F16> __global__ __launch_bounds__(256) void attn_join_kernel(DecodeArgs a)
+// The item that begins in share blockIdx.x and ends in a later one, one of its
+// query heads: o = sum_i 2^(m_i - m) O_i / sum_i 2^(m_i - m) l_i over its
+// shares.  Groups of D / 4 lanes take every so many-th share each and are added
+// in order; a handful of kilobytes per row, bound by latency.
+template <int D, bool F16, int NT> __global__ __launch_bounds__(256) void attn_join_kernel(DecodeArgs a)
 {
-    constexpr int kPer = D / 64;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int64_t row = blockIdx.x;
-    const int seq = (int)(row / (a.cache.hkv * a.G));
-    const int len = clampi(a.lens[seq], 0, a.longest);
-    const int n = (len + a.chunk - 1) / a.chunk;
-    const float *const st = a.stats + 2 * row * a.splits;
+    constexpr int kLanes = D / 4, kGroups = 256 / kLanes;
+    const int me = blockIdx.x, r = blockIdx.y;
+    const int n = a.spans[3 * me], seq = a.spans[3 * me + 1], item = a.spans[3 * me + 2];
+    const int h = item % a.cache.hkv, head = item / a.cache.hkv * 16 * NT + r;
+    if (n == 0 || head >= a.G)
+        return;
+    // share i of the item: slot 1 of the first workgroup, slot 0 of the others
+    auto row_of = [&](int i) { return (int64_t)(2 * (me + i) + (i == 0)) * 16 * NT + r; };
     float top = kLowest;
-    for (int i = lane; i < n; i += 64)
-        top = fmaxf(top, st[2 * i]);
+    for (int i = threadIdx.x & 63; i < n; i += 64)
+        top = fmaxf(top, a.stats[2 * row_of(i)]);
 #pragma unroll
     for (int d = 1; d < 64; d *= 2)
         top = fmaxf(top, __shfl_xor(top, d));
-    float x[kPer] = {}, sum = 0.f;
-#pragma unroll 8
-    for (int i = wave; i < n; i += 4) {
-        const float f = exp2_fast(st[2 * i] - top);
-        const float *const p = a.part + (row * a.splits + i) * D + kPer * lane;
-        sum += f * st[2 * i + 1];
-#pragma unroll
-        for (int c = 0; c < kPer; ++c)
-            x[c] += f * p[c];
+    const int c = 4 * (threadIdx.x % kLanes), group = threadIdx.x / kLanes;
+    f32x4 x = {};
+    float sum = 0.f;
+#pragma unroll 4
+    for (int i = group; i < n; i += kGroups) {
+        const int64_t at = row_of(i);
+        const float f = exp2_fast(a.stats[2 * at] - top);
+        sum += f * a.stats[2 * at + 1];
+        x += f * *reinterpret_cast<const f32x4 *>(a.part + at * D + c);
     }
-    __shared__ float s_x[4][D], s_l[4];
-#pragma unroll
-    for (int c = 0; c < kPer; ++c)
-        s_x[wave][kPer * lane + c] = x[c];
-    if (lane == 0)
-        s_l[wave] = sum;
+    __shared__ __attribute__((aligned(16))) float s_x[kGroups][D];
+    __shared__ float s_l[kGroups];
+    *reinterpret_cast<f32x4 *>(&s_x[group][c]) = x;
+    if (c == 0)
+        s_l[group] = sum;
     __syncthreads();
     if ((int)threadIdx.x < D / 2) {
-        const int c = 2 * threadIdx.x;
-        const float all = s_l[0] + s_l[1] + s_l[2] + s_l[3];
+        const int e = 2 * threadIdx.x;
+        float all = 0.f, u = 0.f, v = 0.f;
+#pragma unroll
+        for (int i = 0; i < kGroups; ++i) {
+            all += s_l[i];
+            u += s_x[i][e];
+            v += s_x[i][e + 1];
+        }
         const float inv = all == 0.f ? 1.f : 1.f / all;
-        const float u = s_x[0][c] + s_x[1][c] + s_x[2][c] + s_x[3][c];
-        const float v = s_x[0][c + 1] + s_x[1][c + 1] + s_x[2][c + 1] + s_x[3][c + 1];
-        *reinterpret_cast<uint32_t *>(a.out + row * D + c) = pack_half_x2<F16>(u * inv, v * inv);
+        const int64_t row = ((int64_t)seq * a.cache.hkv + h) * a.G + head;
+        *reinterpret_cast<uint32_t *>(a.out + row * D + e) = pack_half_x2<F16>(u * inv, v * inv);
     }
 }
 
-template <int D, bool F16, int NT> hipError_t run(const DecodeArgs &a, int seqs, int groups, hipStream_t st)
+template <int D, bool F16, int NT> hipError_t run(const DecodeArgs &a, const DecodePlan &p, hipStream_t st)
 {
-    attn_decode_kernel<D, F16, NT><<<dim3(a.cache.hkv * groups, seqs, a.splits), 64 * kWaves, 0, st>>>(a);
+    if (p.shares == 0) {
+        attn_decode_kernel<D, F16, NT, false><<<dim3(a.cache.hkv * a.groups, a.seqs), 64 * kWaves, 0, st>>>(a);
+        return hipGetLastError();
+    }
+    attn_decode_kernel<D, F16, NT, true><<<(unsigned)p.shares, 64 * kWaves, 0, st>>>(a);
+    if (hipError_t e = hipGetLastError(); e != hipSuccess)
+        return e;
+    attn_join_kernel<D, F16, NT><<<dim3((unsigned)p.shares, std::min(a.G, 16 * NT)), 256, 0, st>>>(a);
     return hipGetLastError();
 }
 
-template <int D, bool F16> hipError_t run_d(const DecodeArgs &a, int seqs, int nt, int groups, hipStream_t st)
+template <int D, bool F16> hipError_t run_d(const DecodeArgs &a, const DecodePlan &p, hipStream_t st)
 {
-    hipError_t e = nt == 1   ? run<D, F16, 1>(a, seqs, groups, st)
-                   : nt == 2 ? run<D, F16, 2>(a, seqs, groups, st)
-                             : run<D, F16, 3>(a, seqs, groups, st);
-    if (e != hipSuccess || a.splits == 1)
-        return e;
-    attn_join_kernel<D, F16><<<dim3((unsigned)(seqs * a.cache.hkv * a.G)), 256, 0, st>>>(a);
-    return hipGetLastError();
+    return p.nt == 1 ? run<D, F16, 1>(a, p, st) : p.nt == 2 ? run<D, F16, 2>(a, p, st) : run<D, F16, 3>(a, p, st);
 }
 
 } // namespace
 
 // Query heads of a key-value head are covered by groups of nt tiles of 16, at
 // most three (the accumulators of more do not fit the registers beside two
-// stages).  The cache's length is cut into chunks so that the grid at the
-// longest length fills the device a few times over, each chunk a whole
-// number of rounds of the waves' tiles.
+// stages).
+// Equal shares cost a look for the share's start, a bubble at each item's end
+// and the join.  A workgroup per item is quicker where an item is two tiles a
+// wave at most (one sequence of 333 tokens, 8 heads: DIRECT us, and SHARE in
+// shares), and for caches of up to 1024 keys where the items fill the device
+// twice (100 sequences of up to 1000 tokens, 8 heads: 52 us, and 60); there the
+// longest item, alone at the end, takes no more than some 20 us.
 DecodePlan plan_decode(int64_t seqs, int64_t hkv, int64_t G, int64_t longest, int cus)
 {
     DecodePlan p;
     const int64_t tiles = (G + 15) / 16;
     p.groups = (tiles + 2) / 3;
     p.nt = (tiles + p.groups - 1) / p.groups;
-    const int64_t round = kWaves * kTile;
-    const int64_t rounds = std::max<int64_t>(1, (longest + round - 1) / round);
-    const int64_t have = std::max<int64_t>(1, seqs * hkv * p.groups), want = 4 * (int64_t)cus;
-    int64_t splits = std::min(rounds, std::max<int64_t>(1, want / have));
-    if (longest <= 2 * round)
-        splits = 1;
-    const int64_t per = (rounds + splits - 1) / splits;
-    p.chunk = per * round;
-    p.splits = (rounds + per - 1) / per;
+    const bool direct = longest <= 512 || (longest <= 1024 && seqs * hkv * p.groups >= 2 * cus);
+    p.shares = direct ? 0 : cus;
     return p;
 }
 
-hipError_t launch_attn_decode(const DecodeArgs &a, int D, bool f16, int64_t seqs, const DecodePlan &p, hipStream_t st)
+hipError_t launch_attn_decode(const DecodeArgs &a, int D, bool f16, const DecodePlan &p, hipStream_t st)
 {
-    const int s = (int)seqs, nt = (int)p.nt, gr = (int)p.groups;
     if (D == 64)
-        return f16 ? run_d<64, true>(a, s, nt, gr, st) : run_d<64, false>(a, s, nt, gr, st);
-    return f16 ? run_d<128, true>(a, s, nt, gr, st) : run_d<128, false>(a, s, nt, gr, st);
+        return f16 ? run_d<64, true>(a, p, st) : run_d<64, false>(a, p, st);
+    return f16 ? run_d<128, true>(a, p, st) : run_d<128, false>(a, p, st);
 }
 
 } // namespace tf

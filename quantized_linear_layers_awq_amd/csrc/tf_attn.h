@@ -17,16 +17,17 @@ struct DecodeArgs {
     PagedCache cache;
     const int32_t *lens;
     uint16_t *out; // [seqs][Hq][D]
-    float *part;   // [seqs][Hq][splits][D], when splits > 1
-    float *stats;  // [seqs][Hq][splits][2]: maximum, sum
-    int G, longest, chunk, splits;
+    float *part;    // [shares][2][16 nt][D]: partial results of items that a share holds in part
+    float *stats;   // [shares][2][16 nt][2]: their maximum and sum
+    int32_t *spans; // [shares][3]: shares of the item that begins here and ends later (0: none), its sequence and number
+    int seqs, G, groups, longest;
     float scale_log2;
 };
 struct DecodePlan {
-    int64_t nt, groups, chunk, splits;
+    int64_t nt, groups, shares; // shares == 0: a workgroup per item
 };
 DecodePlan plan_decode(int64_t seqs, int64_t hkv, int64_t G, int64_t longest, int cus);
-hipError_t launch_attn_decode(const DecodeArgs &a, int D, bool f16, int64_t seqs, const DecodePlan &p, hipStream_t st);
+hipError_t launch_attn_decode(const DecodeArgs &a, int D, bool f16, const DecodePlan &p, hipStream_t st);
 
 // ---- packed prompts ---------------------------------------------------------
 struct PrefillArgs {

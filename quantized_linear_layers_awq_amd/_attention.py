@@ -30,20 +30,21 @@ def _type(t: torch.Tensor, fn: str, name: str) -> int:
         raise ValueError(f"{fn}: {name} must be bfloat16 or float16 (got {t.dtype})") from None
 
 
-def _same(fn: str, dtype, device, **tensors):
-    """Tensors of `dtype` on `device`, contiguous."""
-    for name, t in tensors.items():
-        if t.dtype is not dtype or t.device != device or not t.is_contiguous():
-            raise ValueError(f"{fn}: {name} must be a contiguous {dtype} tensor on {device} "
+def _same(fn: str, names, dtype, index: int, *tensors):
+    """Tensors of `dtype` on device `index`, contiguous; `names` in their order, space-separated."""
+    for t in tensors:
+        if t.dtype is not dtype or t.get_device() != index or not t.is_contiguous():
+            i = next(i for i, u in enumerate(tensors) if u is t)
+            raise ValueError(f"{fn}: {names.split()[i]} must be a contiguous {dtype} tensor on cuda:{index} "
                              f"(got {t.dtype} on {t.device}, strides {tuple(t.stride())})")
 
 
-def _device(t: torch.Tensor, fn: str, name: str):
+def _device(t: torch.Tensor, fn: str, name: str) -> int:
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{fn}: {name} must be a torch.Tensor")
     if not t.is_cuda:
         raise ValueError(f"{fn}: {name} must be a device tensor (got {t.device})")
-    return t.device
+    return t.get_device()
 
 
 class _On:
@@ -51,27 +52,29 @@ class _On:
     stream, so that torch orders the memory's reuse with the call; a call on
     another device than the current one switches to it."""
 
-    def __init__(self, device, stream):
-        self.contexts = []
-        index = device.index
+    __slots__ = ("index", "handle", "contexts")
+
+    def __init__(self, index, stream):
+        self.index = index
+        self.contexts = ()
         if torch._C._cuda_getDevice() != index:
             self._enter(torch.cuda.device(index))
         if stream is None:
             self.handle = torch._C._cuda_getCurrentRawStream(index)
         else:
             self.handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-            self._enter(torch.cuda.stream(torch.cuda.ExternalStream(self.handle, device=device)))
+            self._enter(torch.cuda.stream(torch.cuda.ExternalStream(self.handle, device=torch.device("cuda", index))))
 
     def _enter(self, context):
         context.__enter__()
-        self.contexts.append(context)
+        self.contexts += (context,)
 
     def __enter__(self):
         return self
 
     def __exit__(self, *error):
-        while self.contexts:
-            self.contexts.pop().__exit__(*error)
+        for context in reversed(self.contexts):
+            context.__exit__(*error)
 
 
 def _stride(t: torch.Tensor, fn: str, name: str):
@@ -84,34 +87,31 @@ def _stride(t: torch.Tensor, fn: str, name: str):
     return (token if tokens > 1 else heads * d if token < d else token), (head if heads > 1 else d)
 
 
-def _result(t, shape, dtype, device, fn, name):
-    if t is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    return _given(t, shape, dtype, device, fn, name)
+def _result(t, shape, like, index, fn, name):
+    """The given output, checked, or a new one of `like`'s type and device."""
+    return like.new_empty(shape) if t is None else _given(t, shape, like.dtype, index, fn, name)
 
 
-def _given(t, shape, dtype, device, fn, name):
-    _same(fn, dtype, device, **{name: t})
-    if t.shape != torch.Size(shape):
+def _given(t, shape, dtype, index, fn, name):
+    _same(fn, name, dtype, index, t)
+    if t.shape != shape:
         raise ValueError(f"{fn}: {name} must be {list(shape)} (got {list(t.shape)})")
     return t
 
 
-def _pages(fn, dtype, device, k_pages, v_pages, tables):
-    _same(fn, dtype, device, k_pages=k_pages, v_pages=v_pages)
-    _same(fn, _I32, device, tables=tables)
+def _pages(fn, k_pages, v_pages, tables):
     if k_pages.dim() != 4 or k_pages.shape != v_pages.shape or tables.dim() != 2:
         raise ValueError(f"{fn}: k_pages and v_pages must be [pages][Hkv][page][D] of one shape, tables [seqs][width]")
     return k_pages.shape
 
 
-def _need_workspace(workspace, device, handle, nbytes, fn):
+def _need_workspace(workspace, on, nbytes, fn):
     if nbytes == 0:
         return None, 0
     if workspace is None:
-        workspace = _workspace(device, handle, nbytes)
-    elif workspace.device != device or not workspace.is_contiguous():
-        raise ValueError(f"{fn}: workspace must be a contiguous tensor on {device}")
+        workspace = _workspace(torch.device("cuda", on.index), on.handle, nbytes)
+    elif workspace.get_device() != on.index or not workspace.is_contiguous():
+        raise ValueError(f"{fn}: workspace must be a contiguous tensor on cuda:{on.index}")
     return workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
@@ -122,19 +122,20 @@ def tf_kv_append(qkv, rope, seq, pos, tables, k_pages, v_pages, hq, q=None, stre
     int32 [T]; k_pages, v_pages [pages][Hkv][page][D] are written in place.
     Returns q [T][hq][D]."""
     fn = "tf_kv_append"
-    device = _device(qkv, fn, "qkv")
+    index = _device(qkv, fn, "qkv")
     kind = _type(qkv, fn, "qkv")
-    pages, hkv, page, d = _pages(fn, qkv.dtype, device, k_pages, v_pages, tables)
-    _same(fn, torch.float32, device, rope=rope)
-    _same(fn, _I32, device, seq=seq, pos=pos)
-    tokens = seq.numel()
-    if qkv.dim() != 2 or qkv.shape != (tokens, (hq + 2 * hkv) * d) or (qkv.stride(1) != 1 and qkv.numel()):
-        raise ValueError(f"{fn}: qkv must be [{tokens}][{(hq + 2 * hkv) * d}] with contiguous channels")
+    _same(fn, "k_pages v_pages", qkv.dtype, index, k_pages, v_pages)
+    _same(fn, "seq pos tables", _I32, index, seq, pos, tables)
+    _same(fn, "rope", torch.float32, index, rope)
+    pages, hkv, page, d = _pages(fn, k_pages, v_pages, tables)
+    tokens, wide = seq.numel(), (hq + 2 * hkv) * d
+    if qkv.shape != (tokens, wide) or (qkv.stride(1) != 1 and wide > 1 and tokens):
+        raise ValueError(f"{fn}: qkv must be [{tokens}][{wide}] with contiguous channels")
     if pos.numel() != tokens or rope.dim() != 2 or rope.shape[1] != d:
         raise ValueError(f"{fn}: pos must have {tokens} entries, rope must be [positions][{d}]")
-    with _On(device, stream) as on:
-        q = _result(q, (tokens, hq, d), qkv.dtype, device, fn, "q")
-        _check(_lib().tf_kv_append(kind, qkv.data_ptr(), qkv.stride(0) if tokens > 1 else qkv.shape[1], rope.data_ptr(),
+    with _On(index, stream) as on:
+        q = _result(q, (tokens, hq, d), qkv, index, fn, "q")
+        _check(_lib().tf_kv_append(kind, qkv.data_ptr(), qkv.stride(0) if tokens > 1 else wide, rope.data_ptr(),
                                    rope.shape[0], seq.data_ptr(), pos.data_ptr(), tokens, tables.data_ptr(),
                                    tables.shape[0], tables.shape[1], q.data_ptr(), k_pages.data_ptr(),
                                    v_pages.data_ptr(), pages, page, hq, hkv, d, on.handle), fn)
@@ -154,10 +155,11 @@ def tf_attn_decode(q, k_pages, v_pages, tables, lens, longest, scale=None, out=N
     contiguous), over the first lens[s] tokens of its pages (lens int32 [seqs],
     at most `longest`).  scale defaults to D^-0.5.  Returns [seqs][Hq][D]."""
     fn = "tf_attn_decode"
-    device = _device(q, fn, "q")
+    index = _device(q, fn, "q")
     kind = _type(q, fn, "q")
-    pages, hkv, page, d = _pages(fn, q.dtype, device, k_pages, v_pages, tables)
-    _same(fn, _I32, device, lens=lens)
+    _same(fn, "k_pages v_pages", q.dtype, index, k_pages, v_pages)
+    _same(fn, "tables lens", _I32, index, tables, lens)
+    pages, hkv, page, d = _pages(fn, k_pages, v_pages, tables)
     if q.dim() != 3 or q.shape[2] != d:
         raise ValueError(f"{fn}: q must be [seqs][Hq][{d}]")
     seqs, hq, _ = q.shape
@@ -165,10 +167,9 @@ def tf_attn_decode(q, k_pages, v_pages, tables, lens, longest, scale=None, out=N
         raise ValueError(f"{fn}: lens and tables must have {seqs} rows")
     token, head = _stride(q, fn, "q")
     lib = _lib()
-    with _On(device, stream) as on:
-        out = _result(out, (seqs, hq, d), q.dtype, device, fn, "out")
-        ws, have = _need_workspace(workspace, device, on.handle,
-                                   lib.tf_attn_decode_workspace_bytes(seqs, hq, hkv, d, longest), fn)
+    with _On(index, stream) as on:
+        out = _result(out, (seqs, hq, d), q, index, fn, "out")
+        ws, have = _need_workspace(workspace, on, lib.tf_attn_decode_workspace_bytes(seqs, hq, hkv, d, longest), fn)
         _check(lib.tf_attn_decode(kind, q.data_ptr(), token, head, k_pages.data_ptr(), v_pages.data_ptr(), pages, page,
                                   tables.data_ptr(), tables.shape[1], lens.data_ptr(), out.data_ptr(), seqs, hq, hkv, d,
                                   longest, _scale(scale, d), ws, have, on.handle), fn)
@@ -186,27 +187,28 @@ def tf_attn_prefill(q, k, v, cu_q, cu_k, longest, scale=None, out=None, workspac
     cu_k[s + 1] of k and v (int32 [seqs + 1]), its last token seeing every
     key.  `longest` bounds the new tokens of a sequence.  Returns [T][Hq][D]."""
     fn = "tf_attn_prefill"
-    device = _device(q, fn, "q")
+    index = _device(q, fn, "q")
     kind = _type(q, fn, "q")
-    _same(fn, _I32, device, cu_q=cu_q, cu_k=cu_k)
+    _same(fn, "cu_q cu_k", _I32, index, cu_q, cu_k)
     if q.dim() != 3 or k.dim() != 3 or k.shape != v.shape or k.shape[2] != q.shape[2]:
         raise ValueError(f"{fn}: q must be [T][Hq][D], k and v [keys][Hkv][D] of one shape")
-    if k.dtype is not q.dtype or v.dtype is not q.dtype or k.device != device or v.device != device:
+    if k.dtype is not q.dtype or v.dtype is not q.dtype or k.get_device() != index or v.get_device() != index:
         raise ValueError(f"{fn}: q, k and v must have one type and device")
-    if cu_q.numel() < 1 or cu_q.numel() != cu_k.numel():
+    seqs = cu_q.numel() - 1
+    if seqs < 0 or cu_k.numel() != seqs + 1:
         raise ValueError(f"{fn}: cu_q and cu_k must have seqs + 1 entries")
     tokens, hq, d = q.shape
     keys, hkv, _ = k.shape
     qt, qh = _stride(q, fn, "q")
     kt, kh = _stride(k, fn, "k")
     vt, vh = _stride(v, fn, "v")
-    lib, seqs = _lib(), cu_q.numel() - 1
-    with _On(device, stream) as on:
-        out = _result(out, (tokens, hq, d), q.dtype, device, fn, "out")
-        ws, have = _need_workspace(workspace, device, on.handle,
+    lib = _lib()
+    with _On(index, stream) as on:
+        out = _result(out, (tokens, hq, d), q, index, fn, "out")
+        ws, have = _need_workspace(workspace, on,
                                    lib.tf_attn_prefill_workspace_bytes(seqs, tokens, hq, hkv, d, longest, keys), fn)
         _check(lib.tf_attn_prefill(kind, q.data_ptr(), qt, qh, k.data_ptr(), kt, kh, v.data_ptr(), vt, vh,
-                                      cu_q.data_ptr(), cu_k.data_ptr(), out.data_ptr(), seqs, tokens, keys, hq, hkv, d,
+                                   cu_q.data_ptr(), cu_k.data_ptr(), out.data_ptr(), seqs, tokens, keys, hq, hkv, d,
                                    longest, _scale(scale, d), ws, have, on.handle), fn)
     return out
 
@@ -217,24 +219,25 @@ def tf_attn_prefill_paged(q, k_pages, v_pages, tables, cu_q, lens, longest, scal
     cu_q[s] .. cu_q[s + 1]) over the first lens[s] tokens of the sequences'
     pages, the new ones included.  Returns [T][Hq][D]."""
     fn = "tf_attn_prefill_paged"
-    device = _device(q, fn, "q")
+    index = _device(q, fn, "q")
     kind = _type(q, fn, "q")
-    pages, hkv, page, d = _pages(fn, q.dtype, device, k_pages, v_pages, tables)
-    _same(fn, _I32, device, cu_q=cu_q, lens=lens)
+    _same(fn, "k_pages v_pages", q.dtype, index, k_pages, v_pages)
+    _same(fn, "tables cu_q lens", _I32, index, tables, cu_q, lens)
+    pages, hkv, page, d = _pages(fn, k_pages, v_pages, tables)
     if q.dim() != 3 or q.shape[2] != d:
         raise ValueError(f"{fn}: q must be [T][Hq][{d}]")
-    seqs = lens.numel()
-    if cu_q.numel() != seqs + 1 or tables.shape[0] != seqs:
+    seqs, (rows, width) = lens.numel(), tables.shape
+    if cu_q.numel() != seqs + 1 or rows != seqs:
         raise ValueError(f"{fn}: cu_q must have {seqs + 1} entries, tables {seqs} rows")
     tokens, hq, _ = q.shape
     token, head = _stride(q, fn, "q")
-    lib, width = _lib(), tables.shape[1]
-    with _On(device, stream) as on:
-        out = _result(out, (tokens, hq, d), q.dtype, device, fn, "out")
-        ws, have = _need_workspace(workspace, device, on.handle,
+    lib = _lib()
+    with _On(index, stream) as on:
+        out = _result(out, (tokens, hq, d), q, index, fn, "out")
+        ws, have = _need_workspace(workspace, on,
                                    lib.tf_attn_prefill_workspace_bytes(seqs, tokens, hq, hkv, d, longest, width * page), fn)
         _check(lib.tf_attn_prefill_paged(kind, q.data_ptr(), token, head, k_pages.data_ptr(), v_pages.data_ptr(),
-                                            pages, page, tables.data_ptr(), width, cu_q.data_ptr(), lens.data_ptr(),
+                                         pages, page, tables.data_ptr(), width, cu_q.data_ptr(), lens.data_ptr(),
                                          out.data_ptr(), seqs, tokens, hq, hkv, d, longest, _scale(scale, d), ws, have,
                                          on.handle), fn)
     return out
@@ -249,13 +252,13 @@ def tf_kv_compact_workspace_bytes(pages: int) -> int:
 
 
 def _pool(fn, cache, refs, tables):
-    device = _device(cache, fn, "cache")
+    index = _device(cache, fn, "cache")
     if cache.dim() != 5 or cache.element_size() != 2 or not cache.is_contiguous():
         raise ValueError(f"{fn}: cache must be a contiguous 16-bit tensor [planes][pages][Hkv][page][D]")
-    _same(fn, _I32, device, refs=refs, tables=tables)
+    _same(fn, "refs tables", _I32, index, refs, tables)
     if refs.numel() != cache.shape[1] or tables.dim() != 2:
         raise ValueError(f"{fn}: refs must have {cache.shape[1]} entries, tables must be [seqs][width]")
-    return device
+    return index
 
 
 def tf_kv_fork(cache, refs, tables, lens, parents, children, refs_out=None, tables_out=None, lens_out=None, status=None,
@@ -267,19 +270,19 @@ def tf_kv_fork(cache, refs, tables, lens, parents, children, refs_out=None, tabl
     tensors, or replaces the inputs where none is given.  Returns status, int32 [1]:
     0, or how many free pages were missing (then nothing is forked)."""
     fn = "tf_kv_fork"
-    device = _pool(fn, cache, refs, tables)
-    _same(fn, _I32, device, lens=lens, parents=parents, children=children)
+    index = _pool(fn, cache, refs, tables)
+    _same(fn, "lens parents children", _I32, index, lens, parents, children)
     if lens.numel() != tables.shape[0] or parents.numel() != children.numel():
         raise ValueError(f"{fn}: lens must have {tables.shape[0]} entries, parents and children equally many")
     planes, pages, hkv, page, d = cache.shape
     forks = parents.numel()
     lib = _lib()
-    with _On(device, stream) as on:
-        refs_out = refs if refs_out is None else _given(refs_out, refs.shape, _I32, device, fn, "refs_out")
-        tables_out = tables if tables_out is None else _given(tables_out, tables.shape, _I32, device, fn, "tables_out")
-        lens_out = lens if lens_out is None else _given(lens_out, lens.shape, _I32, device, fn, "lens_out")
-        status = _result(status, (1,), _I32, device, fn, "status")
-        ws, have = _need_workspace(workspace, device, on.handle, lib.tf_kv_fork_workspace_bytes(forks), fn)
+    with _On(index, stream) as on:
+        refs_out = refs if refs_out is None else _given(refs_out, refs.shape, _I32, index, fn, "refs_out")
+        tables_out = tables if tables_out is None else _given(tables_out, tables.shape, _I32, index, fn, "tables_out")
+        lens_out = lens if lens_out is None else _given(lens_out, lens.shape, _I32, index, fn, "lens_out")
+        status = _result(status, (1,), refs, index, fn, "status")
+        ws, have = _need_workspace(workspace, on, lib.tf_kv_fork_workspace_bytes(forks), fn)
         _check(lib.tf_kv_fork(cache.data_ptr(), planes, pages, hkv, page, d, refs.data_ptr(), tables.data_ptr(),
                               lens.data_ptr(), tables.shape[0], tables.shape[1], parents.data_ptr(),
                               children.data_ptr(), forks, refs_out.data_ptr(), tables_out.data_ptr(),
@@ -293,14 +296,14 @@ def tf_kv_compact(cache, refs, tables, refs_out=None, tables_out=None, moved=Non
     state goes to the *_out tensors, or replaces the inputs where none is given.
     Returns moved, int32 [pages]: where each page is now, -1 for free ones."""
     fn = "tf_kv_compact"
-    device = _pool(fn, cache, refs, tables)
+    index = _pool(fn, cache, refs, tables)
     planes, pages, hkv, page, d = cache.shape
     lib = _lib()
-    with _On(device, stream) as on:
-        refs_out = refs if refs_out is None else _given(refs_out, refs.shape, _I32, device, fn, "refs_out")
-        tables_out = tables if tables_out is None else _given(tables_out, tables.shape, _I32, device, fn, "tables_out")
-        moved = _result(moved, (pages,), _I32, device, fn, "moved")
-        ws, have = _need_workspace(workspace, device, on.handle, lib.tf_kv_compact_workspace_bytes(pages), fn)
+    with _On(index, stream) as on:
+        refs_out = refs if refs_out is None else _given(refs_out, refs.shape, _I32, index, fn, "refs_out")
+        tables_out = tables if tables_out is None else _given(tables_out, tables.shape, _I32, index, fn, "tables_out")
+        moved = _result(moved, (pages,), refs, index, fn, "moved")
+        ws, have = _need_workspace(workspace, on, lib.tf_kv_compact_workspace_bytes(pages), fn)
         _check(lib.tf_kv_compact(cache.data_ptr(), planes, pages, hkv, page, d, refs.data_ptr(), tables.data_ptr(),
                                  tables.shape[0], tables.shape[1], refs_out.data_ptr(), tables_out.data_ptr(),
                                  moved.data_ptr(), ws, have, on.handle), fn)

@@ -142,7 +142,7 @@ int check_pool(uint16_t *cache, int64_t planes, int64_t pages, int64_t Hkv, int6
                const int32_t *tables, int64_t seqs, int64_t width, const int32_t *refs_out, const int32_t *tables_out,
                const int32_t *told)
 {
-    if (!count_ok(planes, 0) || !count_ok(pages, 1) || Hkv < 1 || Hkv >= 65536 || page < 1 || page > 1024 || D < 1 ||
+    if (planes < 0 || planes > 65536 || !count_ok(pages, 1) || Hkv < 1 || Hkv >= 65536 || page < 1 || page > 1024 || D < 1 ||
         D > 65536 || seqs < 0 || seqs >= kIntLimit || !count_ok(width, 1) || width >= kIntLimit / page ||
         (Hkv * page * D) >= kIntLimit)
         return TF_ERR_SHAPE;

@@ -1,14 +1,17 @@
-"""Compile the HIP library (libtilefuse.so) for gfx950, in-tree.
+"""Compile the HIP library (libtilefuse.so) for gfx950, in-tree, and the host
+module that marshals the attention and cache calls (_calls.so).
 
-Every source is compiled with hipcc for gfx950 only; packed-fp32 code
-generation is switched off for all device code.  The result lands next to
-this file, where the binding loads it.
+Every HIP source is compiled with hipcc for gfx950 only; packed-fp32 code
+generation is switched off for all device code.  _calls.so is plain C++ against
+torch's headers.  The results land next to this file, where the binding loads
+them.
 """
 
 from __future__ import annotations
 
 import os
 import subprocess
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -17,6 +20,7 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(ROOT, "_build")
 LIB_PATH = os.path.join(HERE, "libtilefuse.so")
+CALLS_PATH = os.path.join(HERE, "_calls.so")
 SOURCES = ("api.hip", "repack.hip", "gemv.hip", "gemm.hip", "gemm256.hip", "probe.hip", "attn_api.hip",
            "attn_decode.hip", "attn_prefill.hip", "kv.hip")
 ARCH = "gfx950"
@@ -35,8 +39,36 @@ def compile_flags() -> list[str]:
             "-I", INCLUDE, "-I", CSRC]
 
 
+def _compile_calls() -> str:
+    import torch
+    from torch.utils.cpp_extension import include_paths
+
+    obj = os.path.join(BUILD_DIR, "torch_calls.o")
+    abi = int(torch._C._GLIBCXX_USE_CXX11_ABI)
+    includes = [x for path in (*include_paths(), sysconfig.get_paths()["include"]) for x in ("-isystem", path)]
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-Wall", f"-D_GLIBCXX_USE_CXX11_ABI={abi}", "-I", INCLUDE, *includes,
+           "-c", os.path.join(CSRC, "torch_calls.cpp"), "-o", obj]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode:
+        raise RuntimeError(f"g++ failed on torch_calls.cpp:\n{r.stdout}{r.stderr}")
+    return obj
+
+
+def _link_calls(obj: str) -> None:
+    from torch.utils.cpp_extension import library_paths
+
+    tmp = CALLS_PATH + f".tmp{os.getpid()}"
+    cmd = ["g++", "-shared", "-fPIC", obj, "-o", tmp, "-L", HERE, "-l:libtilefuse.so",
+           *[f"-L{path}" for path in library_paths()], "-ltorch_python", "-ltorch_cpu", "-ltorch", "-lc10",
+           "-Wl,-rpath,$ORIGIN"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode:
+        raise RuntimeError(f"link failed:\n{r.stdout}{r.stderr}")
+    os.replace(tmp, CALLS_PATH)
+
+
 def build(verbose: bool = False) -> str:
-    """Compile every source and link libtilefuse.so; returns its path."""
+    """Compile every source and link libtilefuse.so and _calls.so; returns the library's path."""
     os.makedirs(BUILD_DIR, exist_ok=True)
 
     def one(src):
@@ -52,6 +84,7 @@ def build(verbose: bool = False) -> str:
 
     jobs = min(len(SOURCES), int(os.environ.get("MAX_JOBS", "8")))
     with ThreadPoolExecutor(max_workers=jobs) as ex:
+        calls = ex.submit(_compile_calls)
         objs = list(ex.map(one, SOURCES))
     tmp = LIB_PATH + f".tmp{os.getpid()}"
     cmd = [hipcc(), f"--offload-arch={ARCH}", "-shared", "-fPIC", *objs, "-o", tmp]
@@ -59,6 +92,7 @@ def build(verbose: bool = False) -> str:
     if r.returncode:
         raise RuntimeError(f"link failed:\n{r.stdout}{r.stderr}")
     os.replace(tmp, LIB_PATH)
+    _link_calls(calls.result())
     return LIB_PATH
 
 

@@ -141,9 +141,19 @@ __device__ __forceinline__ int parent_length(const PoolArgs &a, int p)
 __global__ __launch_bounds__(kScan) void kv_fork_plan_kernel(PoolArgs a)
 {
     __shared__ int shared[kScan / 64];
+    __shared__ int s_page_of[kScan];
     const ForkPlan plan = fork_plan(a);
     const int tid = threadIdx.x;
     int need = 0;
+    int r[kCells]; // the first step's references, on their way while the ranks are found
+    auto read_refs = [&](int p0) {
+#pragma unroll
+        for (int j = 0; j < kCells; ++j) {
+            const int p = p0 + kCells * tid + j;
+            r[j] = p < a.pages ? a.refs[p] : 1;
+        }
+    };
+    read_refs(0);
     for (int i0 = 0; i0 < a.forks; i0 += kScan) {
         const int i = i0 + tid;
         int size = -1, from = -1;
@@ -165,17 +175,17 @@ __global__ __launch_bounds__(kScan) void kv_fork_plan_kernel(PoolArgs a)
             plan.to[i] = wants ? -2 - rank : -1; // a rank until its page is found
         }
     }
-    // ranks are found again below by the page's own rank: page_of[rank]
-    int32_t *const page_of = a.plan + 3 * a.forks;
+    // ranks are found again below by the page's own rank: page_of[rank], in
+    // LDS where they fit
+    int32_t *const page_of = need <= kScan ? s_page_of : a.plan + 3 * a.forks;
     int have = 0;
     for (int p0 = 0; p0 < a.pages; p0 += kScan * kCells) {
-        int r[kCells], count = 0;
+        if (p0)
+            read_refs(p0);
+        int count = 0;
 #pragma unroll
-        for (int j = 0; j < kCells; ++j) {
-            const int p = p0 + kCells * tid + j;
-            r[j] = p < a.pages ? a.refs[p] : 1;
+        for (int j = 0; j < kCells; ++j)
             count += r[j] == 0;
-        }
         int all, rank = scan_exclusive(count, &all, shared) + have;
         have += all;
 #pragma unroll
@@ -225,10 +235,19 @@ __global__ __launch_bounds__(256) void kv_fork_kernel(PoolArgs a, int copies)
         const int units = (size % a.page) * a.D / 8; // 16-byte units of a head
         const uint16_t *src = a.cache + (plane * a.pages + from) * a.hkv * page_elems;
         uint16_t *dst = a.cache + (plane * a.pages + to) * a.hkv * page_elems;
-        for (int u = tid; u < units * a.hkv; u += 256) {
-            const int64_t at = (u / units) * page_elems + 8 * (u % units);
-            *reinterpret_cast<u32x4 *>(dst + at) = load16(src + at);
+        auto at = [&](int u) { return (u / units) * page_elems + 8 * (u % units); };
+        int u = tid;
+        for (; u + 3 * 256 < units * a.hkv; u += 4 * 256) { // four loads in flight
+            u32x4 x[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                x[i] = load16(src + at(u + 256 * i));
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                *reinterpret_cast<u32x4 *>(dst + at(u + 256 * i)) = x[i];
         }
+        for (; u < units * a.hkv; u += 256)
+            *reinterpret_cast<u32x4 *>(dst + at(u)) = load16(src + at(u));
         return;
     }
     b -= copies;

@@ -11,6 +11,10 @@
 // allocates what is None on the current stream, and returns the output; or a
 // number: a tf_status above zero, or minus the bytes of a workspace that is
 // needed and was not given.
+//
+// The GIL is held throughout.  Some calls launch two kernels that hand over a
+// workspace, which is the stream's: two threads that call on one stream must
+// not get between them.
 #include <Python.h>
 
 #include <algorithm>
@@ -171,14 +175,6 @@ PyObject *wrong_count(const char *fn)
 
 PyObject *outcome(int status, const at::Tensor &out) { return status == TF_OK ? THPVariable_Wrap(out) : PyLong_FromLong(status); }
 
-// The GIL is released around each C call: a launch may wait for a full queue.
-template <typename F> int unlocked(F &&f)
-{
-    int status;
-    Py_BEGIN_ALLOW_THREADS status = f();
-    Py_END_ALLOW_THREADS return status;
-}
-
 // qkv, rope, seq, pos, tables, k_pages, v_pages, hq, q, stream
 PyObject *kv_append(PyObject *, PyObject *const *p, Py_ssize_t n)
 {
@@ -197,11 +193,9 @@ PyObject *kv_append(PyObject *, PyObject *const *p, Py_ssize_t n)
         refuse(c.fn, "pos must have " + std::to_string(tokens) + " entries, rope must be [positions][" + std::to_string(g.d) + "]");
     const at::Tensor q = c.result(p[8], "q", {tokens, hq, g.d}, qkv);
     void *const stream = stream_of(p[9]);
-    const int status = unlocked([&] {
-        return tf_kv_append(kind, halves(qkv), tokens > 1 ? qkv.stride(0) : wide, static_cast<const float *>(rope.data_ptr()),
-                            rope.size(0), words(seq), words(pos), tokens, words(g.tables), g.seqs, g.width, halves_out(q),
-                            halves_out(g.k), halves_out(g.v), g.pages, g.page, hq, g.hkv, g.d, stream);
-    });
+    const int status = tf_kv_append(kind, halves(qkv), tokens > 1 ? qkv.stride(0) : wide, static_cast<const float *>(rope.data_ptr()),
+        rope.size(0), words(seq), words(pos), tokens, words(g.tables), g.seqs, g.width, halves_out(q),
+        halves_out(g.k), halves_out(g.v), g.pages, g.page, hq, g.hkv, g.d, stream);
     return outcome(status, q);
     END_HANDLE_TH_ERRORS
 }
@@ -229,11 +223,9 @@ PyObject *attn_decode(PyObject *, PyObject *const *p, Py_ssize_t n)
     const at::Tensor out = c.result(p[7], "out", {seqs, hq, g.d}, q);
     const float scale = scale_of(p[6], g.d);
     void *const stream = stream_of(p[9]);
-    const int status = unlocked([&] {
-        return tf_attn_decode(kind, halves(q), s.token, s.head, halves(g.k), halves(g.v), g.pages, g.page, words(g.tables),
-                              g.width, words(lens), halves_out(out), seqs, hq, g.hkv, g.d, longest, scale, ws.at, ws.bytes,
-                              stream);
-    });
+    const int status = tf_attn_decode(kind, halves(q), s.token, s.head, halves(g.k), halves(g.v), g.pages, g.page, words(g.tables),
+        g.width, words(lens), halves_out(out), seqs, hq, g.hkv, g.d, longest, scale, ws.at, ws.bytes,
+        stream);
     return outcome(status, out);
     END_HANDLE_TH_ERRORS
 }
@@ -263,11 +255,9 @@ PyObject *attn_prefill(PyObject *, PyObject *const *p, Py_ssize_t n)
     const at::Tensor out = c.result(p[7], "out", {tokens, hq, d}, q);
     const float scale = scale_of(p[6], d);
     void *const stream = stream_of(p[9]);
-    const int status = unlocked([&] {
-        return tf_attn_prefill(kind, halves(q), sq.token, sq.head, halves(k), sk.token, sk.head, halves(v), sv.token, sv.head,
-                               words(cu_q), words(cu_k), halves_out(out), seqs, tokens, keys, hq, hkv, d, longest, scale,
-                               ws.at, ws.bytes, stream);
-    });
+    const int status = tf_attn_prefill(kind, halves(q), sq.token, sq.head, halves(k), sk.token, sk.head, halves(v), sv.token, sv.head,
+        words(cu_q), words(cu_k), halves_out(out), seqs, tokens, keys, hq, hkv, d, longest, scale,
+        ws.at, ws.bytes, stream);
     return outcome(status, out);
     END_HANDLE_TH_ERRORS
 }
@@ -296,11 +286,9 @@ PyObject *attn_prefill_paged(PyObject *, PyObject *const *p, Py_ssize_t n)
     const at::Tensor out = c.result(p[8], "out", {tokens, hq, g.d}, q);
     const float scale = scale_of(p[7], g.d);
     void *const stream = stream_of(p[10]);
-    const int status = unlocked([&] {
-        return tf_attn_prefill_paged(kind, halves(q), s.token, s.head, halves(g.k), halves(g.v), g.pages, g.page,
-                                     words(g.tables), g.width, words(cu_q), words(lens), halves_out(out), seqs, tokens, hq,
-                                     g.hkv, g.d, longest, scale, ws.at, ws.bytes, stream);
-    });
+    const int status = tf_attn_prefill_paged(kind, halves(q), s.token, s.head, halves(g.k), halves(g.v), g.pages, g.page,
+        words(g.tables), g.width, words(cu_q), words(lens), halves_out(out), seqs, tokens, hq,
+        g.hkv, g.d, longest, scale, ws.at, ws.bytes, stream);
     return outcome(status, out);
     END_HANDLE_TH_ERRORS
 }
@@ -348,12 +336,10 @@ PyObject *kv_fork(PyObject *, PyObject *const *p, Py_ssize_t n)
         return PyLong_FromLongLong(-(long long)need);
     const at::Tensor status = c.result(p[9], "status", {1}, g.refs);
     void *const stream = stream_of(p[11]);
-    const int done = unlocked([&] {
-        return tf_kv_fork(halves_out(g.cache), g.cache.size(0), g.cache.size(1), g.cache.size(2), g.cache.size(3),
-                          g.cache.size(4), words(g.refs), words(g.tables), words(lens), seqs, g.tables.size(1), words(parents),
-                          words(children), forks, words_out(refs_out), words_out(tables_out), words_out(lens_out),
-                          words_out(status), ws.at, ws.bytes, stream);
-    });
+    const int done = tf_kv_fork(halves_out(g.cache), g.cache.size(0), g.cache.size(1), g.cache.size(2), g.cache.size(3),
+        g.cache.size(4), words(g.refs), words(g.tables), words(lens), seqs, g.tables.size(1), words(parents),
+        words(children), forks, words_out(refs_out), words_out(tables_out), words_out(lens_out),
+        words_out(status), ws.at, ws.bytes, stream);
     return outcome(done, status);
     END_HANDLE_TH_ERRORS
 }
@@ -373,11 +359,9 @@ PyObject *kv_compact(PyObject *, PyObject *const *p, Py_ssize_t n)
         return PyLong_FromLongLong(-(long long)need);
     const at::Tensor moved = c.result(p[5], "moved", {g.cache.size(1)}, g.refs);
     void *const stream = stream_of(p[7]);
-    const int done = unlocked([&] {
-        return tf_kv_compact(halves_out(g.cache), g.cache.size(0), g.cache.size(1), g.cache.size(2), g.cache.size(3),
-                             g.cache.size(4), words(g.refs), words(g.tables), g.tables.size(0), g.tables.size(1),
-                             words_out(refs_out), words_out(tables_out), words_out(moved), ws.at, ws.bytes, stream);
-    });
+    const int done = tf_kv_compact(halves_out(g.cache), g.cache.size(0), g.cache.size(1), g.cache.size(2), g.cache.size(3),
+        g.cache.size(4), words(g.refs), words(g.tables), g.tables.size(0), g.tables.size(1),
+        words_out(refs_out), words_out(tables_out), words_out(moved), ws.at, ws.bytes, stream);
     return outcome(done, moved);
     END_HANDLE_TH_ERRORS
 }

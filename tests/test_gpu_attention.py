@@ -440,3 +440,36 @@ def test_prefill_infinities_past_a_range():
     out = q_.tf_attn_prefill(q, k, v, *ints, new, 0.2)
     torch.cuda.synchronize()
     _check_prefill(q, lambda s, h: (k[:, h].double(), v[:, h].double()), [0, new], [n], hkv, 0.2, out)
+
+
+def test_threads_on_one_stream_share_its_workspace():
+    """Calls of two kernels each from several host threads on the same stream:
+    nothing comes between a call's kernels."""
+    import threading
+
+    _, q_ = gpu_or_skip()
+    hq, hkv, d, page, rounds = 8, 2, 128, 16, 60
+    g = _gen(41)
+    cases = []
+    for lens in ([3000], [700, 5000], [9000, 1, 2000], [1500] * 5):
+        tables, pages = ref.tables_for(lens, page, g)
+        q = _normal(g, (len(lens), hq, d), torch.bfloat16)
+        kp, vp = (_normal(g, (pages, hkv, page, d), torch.bfloat16) for _ in "kv")
+        cases.append((q, kp, vp, tables.to(DEV), torch.tensor(lens, dtype=torch.int32, device=DEV), max(lens)))
+    print("threads on one stream", flush=True)
+    alone = [q_.tf_attn_decode(*c) for c in cases]
+    torch.cuda.synchronize()
+    got, stream = [[] for _ in cases], torch.cuda.current_stream()
+
+    def work(i):
+        for _ in range(rounds):
+            got[i].append(q_.tf_attn_decode(*cases[i], stream=stream))
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(len(cases))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join(timeout=60)
+    torch.cuda.synchronize()
+    for want, outs in zip(alone, got):
+        assert len(outs) == rounds and all(torch.equal(o, want) for o in outs)

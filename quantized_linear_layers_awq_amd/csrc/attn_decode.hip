@@ -20,10 +20,15 @@
 //    query heads), which writes the output.  Long ones: the keys of all
 //    (sequence, head, group) items, counted in rounds of 8 tiles, are laid end
 //    to end and cut into equal shares, one per workgroup and compute unit,
-//    so that ragged lengths leave no tail.  A workgroup
-//    finds its share from a prefix sum of the lengths.  Items that lie whole
-//    in a share are written; the others' fp32 partials are added by
-//    attn_join_kernel in order.  No atomics.
+//    so that ragged lengths leave no tail.  A workgroup finds its share from
+//    a prefix sum of the lengths.  Items that lie whole in a share are
+//    written; the others' fp32 partials are added by attn_join_kernel in
+//    order.  No atomics.
+// Measured, with the reading rate of a plain stream at 7.0 TB/s: 16 contexts of
+// up to 32768 tokens, 8 heads of 128 channels, 173 us (6.5 TB/s); one of 131072
+// 88 us (6.1: the kernel alone runs at 6.5, the join takes 5 us); 48 ragged ones
+// of up to 4096, 4 heads, 47 us (5.1); one of 333 tokens 6.3 us, which is the
+// latency of the chain length, pages, keys, join.
 #include "tf_attn.h"
 
 namespace tf {
@@ -135,189 +140,189 @@ template <int D, bool F16, int NT, bool SHARES> __global__ __launch_bounds__(64 
     // Keys c0 .. c1 - 1 of an item; the result goes to the output (slot < 0)
     // or to a slot of the partial results.
     auto attend = [&](int seq, int item, int c0, int c1, int slot) {
-    const int h = item % a.cache.hkv, group = item / a.cache.hkv;
-    const int tiles = (c1 - c0 + kTile - 1) / kTile;
-    const int row0 = group * 16 * NT; // first query head of the group here
+        const int h = item % a.cache.hkv, group = item / a.cache.hkv;
+        const int tiles = (c1 - c0 + kTile - 1) / kTile;
+        const int row0 = group * 16 * NT; // first query head of the group here
 
-    // Q^T operands: column n is head row0 + 16 nt + n
-    u32x4 q[NT][kSteps];
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-        const int r = min(row0 + 16 * nt + n, a.G - 1);
-        const uint16_t *p = a.q + seq * a.q_token + (int64_t)(h * a.G + r) * a.q_head + 8 * g;
-#pragma unroll
-        for (int s = 0; s < kSteps; ++s)
-            q[nt][s] = load16(p + 32 * s);
-    }
-
-    const int32_t *table = a.cache.tables + (int64_t)seq * a.cache.width;
-    const int page_mask = (1 << a.cache.page_shift) - 1;
-    const int64_t page_elems = (int64_t)D << a.cache.page_shift;
-
-    // lane L: the page of 16-key run L % 2 of this wave's tile it0 + L / 2
-    auto page_ids = [&](int it0) {
-        const int key = c0 + kTile * (wave + kWaves * (it0 + (lane >> 1))) + 16 * (lane & 1);
-        int id = -1;
-        if (key < a.longest) // not c1: the length may still be on its way
-            id = table[key >> a.cache.page_shift];
-        return key < c1 && id < a.cache.pages ? id : -1;
-    };
-    const uint32_t k_off = n * kRow + 16 * g, v_off = 16 * lane;
-    auto load = [&](Stage<D> &st, int it, int ids) {
-        const int key0 = c0 + kTile * (wave + kWaves * it);
-#pragma unroll
-        for (int sub = 0; sub < 2; ++sub) {
-            const int key = key0 + 16 * sub;
-            const int id = __builtin_amdgcn_readlane(ids, (2 * it + sub) & 63);
-            const int rows = id < 0 ? 0 : rows_before(c1, key);
-            const int64_t at = ((int64_t)max(id, 0) * a.cache.hkv + h) * page_elems + (int64_t)(key & page_mask) * D;
-            const Rsrc kr = make_rsrc_n(a.cache.k + at, rows * kRow), vr = make_rsrc_n(a.cache.v + at, rows * kRow);
-#pragma unroll
-            for (int s = 0; s < kSteps; ++s)
-                st.k[sub][s] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(kr, k_off + 64 * s, 0, kStream));
-#pragma unroll
-            for (int s = 0; s < kSteps; ++s)
-                st.v[sub][s] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(vr, v_off + 1024 * s, 0, kStream));
-        }
-    };
-
-    f32x4 o[NT][kTiles] = {}, l[NT] = {};
-    float m[NT];
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-        m[nt] = kLowest;
-    auto compute = [&](const Stage<D> &st, int it) {
-#pragma unroll
-        for (int sub = 0; sub < 2; ++sub)
-#pragma unroll
-            for (int s = 0; s < kSteps; ++s) {
-                const int r = 16 * sub + kRowsPerLoad * s + wr_row;
-                *reinterpret_cast<u32x4 *>(vbuf + r * kRow + 16 * (wr_unit ^ v_swz<D>(r))) = st.v[sub][s];
-            }
-        const int key0 = c0 + kTile * (wave + kWaves * it);
-        u32x4 p[NT];
+        // Q^T operands: column n is head row0 + 16 nt + n
+        u32x4 q[NT][kSteps];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-            f32x4 x[2] = {};
+            const int r = min(row0 + 16 * nt + n, a.G - 1);
+            const uint16_t *p = a.q + seq * a.q_token + (int64_t)(h * a.G + r) * a.q_head + 8 * g;
+#pragma unroll
+            for (int s = 0; s < kSteps; ++s)
+                q[nt][s] = load16(p + 32 * s);
+        }
+
+        const int32_t *table = a.cache.tables + (int64_t)seq * a.cache.width;
+        const int page_mask = (1 << a.cache.page_shift) - 1;
+        const int64_t page_elems = (int64_t)D << a.cache.page_shift;
+
+        // lane L: the page of 16-key run L % 2 of this wave's tile it0 + L / 2
+        auto page_ids = [&](int it0) {
+            const int key = c0 + kTile * (wave + kWaves * (it0 + (lane >> 1))) + 16 * (lane & 1);
+            int id = -1;
+            if (key < a.longest) // not c1: the length may still be on its way
+                id = table[key >> a.cache.page_shift];
+            return key < c1 && id < a.cache.pages ? id : -1;
+        };
+        const uint32_t k_off = n * kRow + 16 * g, v_off = 16 * lane;
+        auto load = [&](Stage<D> &st, int it, int ids) {
+            const int key0 = c0 + kTile * (wave + kWaves * it);
+#pragma unroll
+            for (int sub = 0; sub < 2; ++sub) {
+                const int key = key0 + 16 * sub;
+                const int id = __builtin_amdgcn_readlane(ids, (2 * it + sub) & 63);
+                const int rows = id < 0 ? 0 : rows_before(c1, key);
+                const int64_t at = ((int64_t)max(id, 0) * a.cache.hkv + h) * page_elems + (int64_t)(key & page_mask) * D;
+                const Rsrc kr = make_rsrc_n(a.cache.k + at, rows * kRow), vr = make_rsrc_n(a.cache.v + at, rows * kRow);
+#pragma unroll
+                for (int s = 0; s < kSteps; ++s)
+                    st.k[sub][s] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(kr, k_off + 64 * s, 0, kStream));
+#pragma unroll
+                for (int s = 0; s < kSteps; ++s)
+                    st.v[sub][s] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(vr, v_off + 1024 * s, 0, kStream));
+            }
+        };
+
+        f32x4 o[NT][kTiles] = {}, l[NT] = {};
+        float m[NT];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+            m[nt] = kLowest;
+        auto compute = [&](const Stage<D> &st, int it) {
 #pragma unroll
             for (int sub = 0; sub < 2; ++sub)
 #pragma unroll
-                for (int s = 0; s < kSteps; ++s)
-                    x[sub] = mfma16x16x32<F16>(st.k[sub][s], q[nt][s], x[sub]);
-            if (key0 + kTile > c1) {
+                for (int s = 0; s < kSteps; ++s) {
+                    const int r = 16 * sub + kRowsPerLoad * s + wr_row;
+                    *reinterpret_cast<u32x4 *>(vbuf + r * kRow + 16 * (wr_unit ^ v_swz<D>(r))) = st.v[sub][s];
+                }
+            const int key0 = c0 + kTile * (wave + kWaves * it);
+            u32x4 p[NT];
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    if (key0 + 16 * (i >> 2) + 4 * g + (i & 3) >= c1)
-                        x[i >> 2][i & 3] = -INFINITY;
+            for (int nt = 0; nt < NT; ++nt) {
+                f32x4 x[2] = {};
+#pragma unroll
+                for (int sub = 0; sub < 2; ++sub)
+#pragma unroll
+                    for (int s = 0; s < kSteps; ++s)
+                        x[sub] = mfma16x16x32<F16>(st.k[sub][s], q[nt][s], x[sub]);
+                if (key0 + kTile > c1) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        if (key0 + 16 * (i >> 2) + 4 * g + (i & 3) >= c1)
+                            x[i >> 2][i & 3] = -INFINITY;
+                }
+                float top = fmaxf(fmaxf(fmaxf(x[0][0], x[0][1]), fmaxf(x[0][2], x[0][3])),
+                                  fmaxf(fmaxf(x[1][0], x[1][1]), fmaxf(x[1][2], x[1][3])));
+                top = max_swap32(max_swap16(top)) * a.scale_log2 - kHeadroom<F16>;
+                if (__builtin_amdgcn_ballot_w64(top > m[nt] + kRescaleSlack)) {
+                    const float to = fmaxf(m[nt], top), f = exp2_fast(m[nt] - to);
+                    m[nt] = to;
+                    l[nt] *= f;
+#pragma unroll
+                    for (int t = 0; t < kTiles; ++t)
+                        o[nt][t] *= f;
+                }
+                // P rounds to the inputs' type for the MFMA; the sum is taken over the
+                // rounded values (a product with ones), so that rounding cancels
+                // where a row's weight sits on few keys
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    p[nt][j] = pack_half_x2<F16>(exp2_fast(x[j >> 1][2 * (j & 1)] * a.scale_log2 - m[nt]),
+                                                 exp2_fast(x[j >> 1][2 * (j & 1) + 1] * a.scale_log2 - m[nt]));
+                l[nt] = mfma16x16x32<F16>(ones, p[nt], l[nt]);
             }
-            float top = fmaxf(fmaxf(fmaxf(x[0][0], x[0][1]), fmaxf(x[0][2], x[0][3])),
-                              fmaxf(fmaxf(x[1][0], x[1][1]), fmaxf(x[1][2], x[1][3])));
-            top = max_swap32(max_swap16(top)) * a.scale_log2 - kHeadroom<F16>;
-            if (__builtin_amdgcn_ballot_w64(top > m[nt] + kRescaleSlack)) {
-                const float to = fmaxf(m[nt], top), f = exp2_fast(m[nt] - to);
-                m[nt] = to;
-                l[nt] *= f;
+#pragma unroll
+            for (int t = 0; t < kTiles; ++t) {
+                const u32x2 lo = lds_read_tr(vbuf + tr[t]), hi = lds_read_tr(vbuf + tr[t] + 16 * kRow);
+                const u32x4 v = {lo[0], lo[1], hi[0], hi[1]};
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+                    o[nt][t] = mfma16x16x32<F16>(v, p[nt], o[nt][t]);
+            }
+        };
+
+        // this wave's tiles: wave, wave + 8, ...; two stages, the loads of one in
+        // flight while the other is computed
+        const int mine = tiles > wave ? (tiles - wave + kWaves - 1) / kWaves : 0;
+        if constexpr (D == 128 && NT > 1) {
+            // more heads: the registers hold one stage beside the accumulators, and
+            // the device's other waves cover its loads
+            int ids = -1;
+            for (int it = 0; it < mine; ++it) {
+                if ((it & 31) == 0)
+                    ids = page_ids(it);
+                Stage<D> s0;
+                load(s0, it, ids);
+                compute(s0, it);
+            }
+        } else if (mine > 0) {
+            Stage<D> s0, s1;
+            int ids = page_ids(0);
+            load(s0, 0, ids);
+            for (int it = 0; it < mine; it += 2) {
+                if (it + 1 < mine)
+                    load(s1, it + 1, ids);
+                compute(s0, it);
+                if (it + 2 < mine) {
+                    if (((it + 2) & 31) == 0)
+                        ids = page_ids(it + 2);
+                    load(s0, it + 2, ids);
+                }
+                if (it + 1 < mine)
+                    compute(s1, it + 1);
+            }
+        }
+
+        // join the waves, 16 heads at a time
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            const int heads = min(16, a.G - row0 - 16 * nt);
+            if (heads <= 0)
+                break;
+            __syncthreads();
+            float *const mine_o = reinterpret_cast<float *>(lds + wave * kWaveBytes);
+            if (n < heads) {
 #pragma unroll
                 for (int t = 0; t < kTiles; ++t)
-                    o[nt][t] *= f;
+                    *reinterpret_cast<f32x4 *>(mine_o + n * D + 4 * ((4 * t + g) ^ n)) = o[nt][t]; // 4-float units, XORed
+                                                                                                   // by head: no bank conflicts
+                if (g == 0) {
+                    s_m[wave][n] = m[nt];
+                    s_l[wave][n] = l[nt][0];
+                }
             }
-            // P rounds to the inputs' type for the MFMA; the sum is taken over the
-            // rounded values (a product with ones), so that rounding cancels
-            // where a row's weight sits on few keys
+            __syncthreads();
+            for (int u = threadIdx.x; u < heads * (D / 2); u += 64 * kWaves) {
+                const int r = u / (D / 2), c = 2 * (u % (D / 2));
+                float top = s_m[0][r];
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                p[nt][j] = pack_half_x2<F16>(exp2_fast(x[j >> 1][2 * (j & 1)] * a.scale_log2 - m[nt]),
-                                             exp2_fast(x[j >> 1][2 * (j & 1) + 1] * a.scale_log2 - m[nt]));
-            l[nt] = mfma16x16x32<F16>(ones, p[nt], l[nt]);
-        }
+                for (int w = 1; w < kWaves; ++w)
+                    top = fmaxf(top, s_m[w][r]);
+                float sum = 0.f, x = 0.f, y = 0.f;
 #pragma unroll
-        for (int t = 0; t < kTiles; ++t) {
-            const u32x2 lo = lds_read_tr(vbuf + tr[t]), hi = lds_read_tr(vbuf + tr[t] + 16 * kRow);
-            const u32x4 v = {lo[0], lo[1], hi[0], hi[1]};
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-                o[nt][t] = mfma16x16x32<F16>(v, p[nt], o[nt][t]);
-        }
-    };
-
-    // this wave's tiles: wave, wave + 8, ...; two stages, the loads of one in
-    // flight while the other is computed
-    const int mine = tiles > wave ? (tiles - wave + kWaves - 1) / kWaves : 0;
-    if constexpr (D == 128 && NT > 1) {
-        // more heads: the registers hold one stage beside the accumulators, and
-        // the device's other waves cover its loads
-        int ids = -1;
-        for (int it = 0; it < mine; ++it) {
-            if ((it & 31) == 0)
-                ids = page_ids(it);
-            Stage<D> s0;
-            load(s0, it, ids);
-            compute(s0, it);
-        }
-    } else if (mine > 0) {
-        Stage<D> s0, s1;
-        int ids = page_ids(0);
-        load(s0, 0, ids);
-        for (int it = 0; it < mine; it += 2) {
-            if (it + 1 < mine)
-                load(s1, it + 1, ids);
-            compute(s0, it);
-            if (it + 2 < mine) {
-                if (((it + 2) & 31) == 0)
-                    ids = page_ids(it + 2);
-                load(s0, it + 2, ids);
-            }
-            if (it + 1 < mine)
-                compute(s1, it + 1);
-        }
-    }
-
-    // join the waves, 16 heads at a time
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-        const int heads = min(16, a.G - row0 - 16 * nt);
-        if (heads <= 0)
-            break;
-        __syncthreads();
-        float *const mine_o = reinterpret_cast<float *>(lds + wave * kWaveBytes);
-        if (n < heads) {
-#pragma unroll
-            for (int t = 0; t < kTiles; ++t)
-                *reinterpret_cast<f32x4 *>(mine_o + n * D + 4 * ((4 * t + g) ^ n)) = o[nt][t]; // 4-float units, XORed
-                                                                                               // by head: no bank conflicts
-            if (g == 0) {
-                s_m[wave][n] = m[nt];
-                s_l[wave][n] = l[nt][0];
+                for (int w = 0; w < kWaves; ++w) {
+                    const float f = exp2_fast(s_m[w][r] - top);
+                    const float *const p = reinterpret_cast<const float *>(lds + w * kWaveBytes) + r * D + 4 * ((c >> 2) ^ r) + (c & 3);
+                    sum += f * s_l[w][r];
+                    x += f * p[0];
+                    y += f * p[1];
+                }
+                if (slot < 0) {
+                    const int64_t at = (int64_t)seq * a.cache.hkv * a.G + h * a.G + row0 + 16 * nt + r;
+                    const float inv = sum == 0.f ? 1.f : 1.f / sum;
+                    *reinterpret_cast<uint32_t *>(a.out + at * D + c) = pack_half_x2<F16>(x * inv, y * inv);
+                } else {
+                    const int64_t at = (int64_t)slot * 16 * NT + 16 * nt + r;
+                    *reinterpret_cast<f32x2 *>(a.part + at * D + c) = f32x2{x, y};
+                    if (c == 0)
+                        *reinterpret_cast<f32x2 *>(a.stats + 2 * at) = f32x2{top, sum};
+                }
             }
         }
-        __syncthreads();
-        for (int u = threadIdx.x; u < heads * (D / 2); u += 64 * kWaves) {
-            const int r = u / (D / 2), c = 2 * (u % (D / 2));
-            float top = s_m[0][r];
-#pragma unroll
-            for (int w = 1; w < kWaves; ++w)
-                top = fmaxf(top, s_m[w][r]);
-            float sum = 0.f, x = 0.f, y = 0.f;
-#pragma unroll
-            for (int w = 0; w < kWaves; ++w) {
-                const float f = exp2_fast(s_m[w][r] - top);
-                const float *const p = reinterpret_cast<const float *>(lds + w * kWaveBytes) + r * D + 4 * ((c >> 2) ^ r) + (c & 3);
-                sum += f * s_l[w][r];
-                x += f * p[0];
-                y += f * p[1];
-            }
-            if (slot < 0) {
-                const int64_t at = (int64_t)seq * a.cache.hkv * a.G + h * a.G + row0 + 16 * nt + r;
-                const float inv = sum == 0.f ? 1.f : 1.f / sum;
-                *reinterpret_cast<uint32_t *>(a.out + at * D + c) = pack_half_x2<F16>(x * inv, y * inv);
-            } else {
-                const int64_t at = (int64_t)slot * 16 * NT + 16 * nt + r;
-                *reinterpret_cast<f32x2 *>(a.part + at * D + c) = f32x2{x, y};
-                if (c == 0)
-                    *reinterpret_cast<f32x2 *>(a.stats + 2 * at) = f32x2{top, sum};
-            }
-        }
-    }
     };
 
     if constexpr (!SHARES) {
@@ -447,8 +452,8 @@ template <int D, bool F16> hipError_t run_d(const DecodeArgs &a, const DecodePla
 // stages).
 // Equal shares cost a look for the share's start, a bubble at each item's end
 // and the join.  A workgroup per item is quicker where an item is two tiles a
-// wave at most (one sequence of 333 tokens, 8 heads: DIRECT us, and SHARE in
-// shares), and for caches of up to 1024 keys where the items fill the device
+// wave at most (one sequence, 8 heads: 8.0 us for 512 tokens, and 11.4 for 513
+// in shares; past that each tile a wave adds 2.5 us), and for caches of up to 1024 keys where the items fill the device
 // twice (100 sequences of up to 1000 tokens, 8 heads: 52 us, and 60); there the
 // longest item, alone at the end, takes no more than some 20 us.
 DecodePlan plan_decode(int64_t seqs, int64_t hkv, int64_t G, int64_t longest, int cus)

@@ -7,19 +7,24 @@
 // G = Hq / Hkv query heads j of a key-value head.  The last new token sees
 // every key; a token that sees none (more queries than keys) gives zeros.
 //
-// What bounds it: 4 D operations per visible (token, key, head), on MFMAs;
-// beside them one exponential per score, which the vector unit issues at a
-// quarter of its rate -- for D = 128 about as long as the products take.
+// What bounds it: 4 D operations per visible (token, key, head), on MFMAs, at
+// the clock that the board's power limit leaves them; beside them one
+// exponential per score and some four other vector instructions.
 //  - The rows of one (sequence, key-value head) are its tokens times its G
 //    heads, token-major, so heads that share keys share tiles of them for any
 //    G, and a tile of rows spans few tokens (little waste at the diagonal).
 //    A workgroup of 4 waves takes 128 rows, 32 per wave, one row per MFMA
-//    column (32x32x16).
+//    column (32x32x16); two workgroups run on a compute unit.  (64 rows a
+//    wave, one wave a SIMD, halves the reads of LDS but left nothing to run
+//    in a wave's waits: 8192 tokens 655 us, and 512 so; 8 waves sharing the
+//    tiles of 256 rows: 503 for those, but a third more where rows are few.)
 //  - K and V come in tiles of 64 keys by LDS-DMA, two buffers each, the next
 //    tile's copies running while this one is computed: one barrier per tile.
 //    Units of 16 bytes are XOR-swizzled by row on the way in, K so that 16
-//    rows read at one channel fall into 16 bank groups, V so that the
-//    transpose reads do.
+//    rows read at one channel, V so that 4 rows of 64 bytes read by half a
+//    wave fall on all 64 banks: no conflicts (by counter).
+//  - The scores of the next tile are computed beside this tile's exponentials,
+//    its maximum beside the products with V.
 //  - Wave w copies rows 16 w .. 16 w + 15, which lie in one page (pages hold a
 //    multiple of 16 tokens): one page id per wave and tile.
 //  - Workgroups that run side by side share keys and values in their XCD's L2:
@@ -28,6 +33,12 @@
 //    sequences of up to 6000 tokens, 64/8 heads: 601 us, and 1029 with all
 //    four side by side).
 //  - Few rows behind many keys: the keys are cut into ranges and joined.
+// Measured: one prompt of 8192 tokens, 32/8 heads of 128, 500 to 513 us (1070
+// to 1100 TFLOP/s; a library product of 8192 x 8192 matrices runs at 1116, of
+// 16384 at 1348), MFMAs busy 55 % of 1.87 GHz.  Without the exponentials, the
+// maximum and the sum the same loop takes 480: the matrix units and the power
+// they draw bound it.  For 64 channels, with as many exponentials for half the
+// products, the vector unit does: 71/1 heads, 3 prompts of up to 2048, 690.
 #include "tf_attn.h"
 
 namespace tf {
@@ -38,7 +49,7 @@ constexpr int kWaves = 4;
 constexpr int kKeys = 64;
 constexpr int kMinRange = 4;   // tiles of a range of keys, at least
 constexpr int kMaxSplits = 16; // ranges
-constexpr int64_t kL2Share = 3 << 20;
+constexpr int64_t kL2Share = 3 << 20; // bytes of an XCD's 4 MiB for the keys and values in use
 
 // tiles of a range when the keys of a sequence are cut into `splits`
 __device__ __forceinline__ int prefill_range(int keys, int splits)

@@ -2,8 +2,8 @@
 // (include/tilefuse_attention.h), as a Python module.  These calls stand
 // between two linears of a decode step and their kernels take 3 to 10 us at
 // the smallest sizes, less than checking two dozen attributes and converting
-// as many arguments takes in Python: a call through ctypes held the GPU up at
-// 10 us, one through here at CALLTIME.
+// as many arguments takes in Python: a call through ctypes took the host 10 us,
+// one through here takes 4.8, of which the launch is 3.3.
 //
 // Each function takes its C call's tensors and sizes by position, then the
 // output(s) or None, the workspace or None, the stream handle.  It checks what

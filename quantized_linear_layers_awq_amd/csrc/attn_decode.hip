@@ -51,60 +51,65 @@ template <int D> struct Stage {
 
 template <int D> constexpr int v_swz(int row) { return D == 128 ? 2 * (row & 7) : 2 * ((row >> 1) & 3); }
 
-// The position of a workgroup's share: the sequence it begins in, and the
-// rounds of the sequences before that one.
+// Where a workgroup's share begins: the sequence, its length, and the rounds of
+// the sequences before it (one item each; the launch keeps the rounds of all
+// items below 2^31).
 struct Start {
-    int64_t rounds; // of all sequences, one item each
-    int64_t before;
-    int seq;
+    int rounds; // of all sequences
+    int before, seq, len;
 };
 
 __device__ __forceinline__ int rounds_of(int len, int round) { return (len + round - 1) / round; }
 
-// Finds rounds, and the sequence of the unit-th round of an item (unit(rounds)
-// names it; past the end: seq = seqs).  Every thread takes a strip of sequences.
+// Finds rounds, and the sequence that holds round unit(rounds) of them (none
+// past the end: seq = seqs).  Every thread takes a strip of sequences.
 template <int THREADS, typename Unit> __device__ __forceinline__ Start find_start(const DecodeArgs &a, int round, Unit unit)
 {
-    __shared__ int64_t s_sum[THREADS / 64];
-    __shared__ int64_t s_before;
-    __shared__ int s_seq;
+    __shared__ int s_sum[THREADS / 64], s_found[3];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int strip = (a.seqs + THREADS - 1) / THREADS;
     const int first = min(tid * strip, a.seqs), end = min(first + strip, a.seqs);
-    int64_t sum = 0;
-    for (int s = first; s < end; ++s)
-        sum += rounds_of(clampi(a.lens[s], 0, a.longest), round);
-    int64_t in = sum;
+    int sum = 0, len = 0;
+    for (int s = first; s < end; ++s) {
+        len = clampi(a.lens[s], 0, a.longest);
+        sum += rounds_of(len, round);
+    }
+    int in = sum;
 #pragma unroll
     for (int d = 1; d < 64; d *= 2) {
-        const int64_t y = __shfl_up(in, d);
+        const int y = __shfl_up(in, d);
         in += lane >= d ? y : 0;
     }
     if (lane == 63)
         s_sum[wave] = in;
     if (tid == 0)
-        s_seq = a.seqs;
+        s_found[0] = a.seqs;
     __syncthreads();
-    int64_t before = in - sum, all = 0;
+    int before = in - sum, all = 0;
 #pragma unroll
     for (int w = 0; w < THREADS / 64; ++w) {
-        before += w < wave ? s_sum[w] : 0;
-        all += s_sum[w];
+        const int x = s_sum[w];
+        before += w < wave ? x : 0;
+        all += x;
     }
-    const int64_t at = unit(all);
+    const int at = unit(all);
     if (before <= at && at < before + sum) {
         int s = first;
-        for (;; ++s) {
-            const int r = rounds_of(clampi(a.lens[s], 0, a.longest), round);
-            if (at < before + r)
-                break;
-            before += r;
-        }
-        s_seq = s;
-        s_before = before;
+        if (strip > 1) // the strip's sequence that holds it
+            for (;; ++s) {
+                len = clampi(a.lens[s], 0, a.longest);
+                const int r = rounds_of(len, round);
+                if (at < before + r)
+                    break;
+                before += r;
+            }
+        s_found[0] = s;
+        s_found[1] = before;
+        s_found[2] = len;
     }
     __syncthreads();
-    return {all, s_before, __builtin_amdgcn_readfirstlane(s_seq)};
+    return {all, __builtin_amdgcn_readfirstlane(s_found[1]), __builtin_amdgcn_readfirstlane(s_found[0]),
+            __builtin_amdgcn_readfirstlane(s_found[2])};
 }
 
 // SHARES: equal shares of all keys, else one item of one sequence
@@ -116,7 +121,7 @@ template <int D, bool F16, int NT, bool SHARES> __global__ __launch_bounds__(64 
     constexpr int kChunks = D / 8;   // 16-byte units of a row
     constexpr int kRowsPerLoad = 1024 / kRow;
     constexpr int kWaveBytes = kTile * kRow; // V of a tile; in the join, 16 heads of D floats
-    constexpr int kRound = kWaves * kTile;
+    const int waves = SHARES ? a.waves : kWaves, round = waves * kTile; // keys of a round
     static_assert(kWaveBytes == 16 * D * 4, "the join reuses the V buffers");
     __shared__ __attribute__((aligned(16))) uint8_t lds[kWaves * kWaveBytes];
     __shared__ float s_m[kWaves][16], s_l[kWaves][16];
@@ -161,7 +166,7 @@ template <int D, bool F16, int NT, bool SHARES> __global__ __launch_bounds__(64 
 
         // lane L: the page of 16-key run L % 2 of this wave's tile it0 + L / 2
         auto page_ids = [&](int it0) {
-            const int key = c0 + kTile * (wave + kWaves * (it0 + (lane >> 1))) + 16 * (lane & 1);
+            const int key = c0 + kTile * (wave + waves * (it0 + (lane >> 1))) + 16 * (lane & 1);
             int id = -1;
             if (key < a.longest) // not c1: the length may still be on its way
                 id = table[key >> a.cache.page_shift];
@@ -169,7 +174,7 @@ template <int D, bool F16, int NT, bool SHARES> __global__ __launch_bounds__(64 
         };
         const uint32_t k_off = n * kRow + 16 * g, v_off = 16 * lane;
         auto load = [&](Stage<D> &st, int it, int ids) {
-            const int key0 = c0 + kTile * (wave + kWaves * it);
+            const int key0 = c0 + kTile * (wave + waves * it);
 #pragma unroll
             for (int sub = 0; sub < 2; ++sub) {
                 const int key = key0 + 16 * sub;
@@ -199,7 +204,7 @@ template <int D, bool F16, int NT, bool SHARES> __global__ __launch_bounds__(64 
                     const int r = 16 * sub + kRowsPerLoad * s + wr_row;
                     *reinterpret_cast<u32x4 *>(vbuf + r * kRow + 16 * (wr_unit ^ v_swz<D>(r))) = st.v[sub][s];
                 }
-            const int key0 = c0 + kTile * (wave + kWaves * it);
+            const int key0 = c0 + kTile * (wave + waves * it);
             u32x4 p[NT];
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
@@ -245,9 +250,8 @@ template <int D, bool F16, int NT, bool SHARES> __global__ __launch_bounds__(64 
             }
         };
 
-        // this wave's tiles: wave, wave + 8, ...; two stages, the loads of one in
-        // flight while the other is computed
-        const int mine = tiles > wave ? (tiles - wave + kWaves - 1) / kWaves : 0;
+        // this wave's tiles: wave, wave + waves, ...
+        const int mine = tiles > wave && wave < waves ? (tiles - wave + waves - 1) / waves : 0;
         if constexpr (D == 128 && NT > 1) {
             // more heads: the registers hold one stage beside the accumulators, and
             // the device's other waves cover its loads
@@ -255,25 +259,25 @@ template <int D, bool F16, int NT, bool SHARES> __global__ __launch_bounds__(64 
             for (int it = 0; it < mine; ++it) {
                 if ((it & 31) == 0)
                     ids = page_ids(it);
-                Stage<D> s0;
-                load(s0, it, ids);
-                compute(s0, it);
+                Stage<D> now;
+                load(now, it, ids);
+                compute(now, it);
             }
         } else if (mine > 0) {
-            Stage<D> s0, s1;
+            // the loads of one stage in flight while the other is computed; a
+            // copy of the stage costs less than a second copy of the code
             int ids = page_ids(0);
-            load(s0, 0, ids);
-            for (int it = 0; it < mine; it += 2) {
+            Stage<D> now;
+            load(now, 0, ids);
+#pragma unroll 1
+            for (int it = 0; it < mine; ++it) {
+                if (((it + 1) & 31) == 0)
+                    ids = page_ids(it + 1);
+                Stage<D> next = now;
                 if (it + 1 < mine)
-                    load(s1, it + 1, ids);
-                compute(s0, it);
-                if (it + 2 < mine) {
-                    if (((it + 2) & 31) == 0)
-                        ids = page_ids(it + 2);
-                    load(s0, it + 2, ids);
-                }
-                if (it + 1 < mine)
-                    compute(s1, it + 1);
+                    load(next, it + 1, ids);
+                compute(now, it);
+                now = next;
             }
         }
 
@@ -335,38 +339,34 @@ template <int D, bool F16, int NT, bool SHARES> __global__ __launch_bounds__(64 
             if (a.lens[s] <= 0 || a.longest == 0)
                 for (int64_t u = threadIdx.x; u < (int64_t)a.cache.hkv * a.G * (D / 8); u += 64 * kWaves)
                     reinterpret_cast<u32x4 *>(a.out)[(int64_t)s * a.cache.hkv * a.G * (D / 8) + u] = u32x4{};
-        int64_t per = 0;
-        const Start from = find_start<64 * kWaves>(a, kRound, [&](int64_t all) {
-            per = (all * items + gridDim.x - 1) / gridDim.x;
+        int per = 0;
+        const Start from = find_start<64 * kWaves>(a, round, [&](int all) {
+            per = (all * items + (int)gridDim.x - 1) / (int)gridDim.x;
             return me * per / items;
         });
-        const int64_t end = min(from.rounds * items, (me + 1) * per); // in rounds of items
-        int64_t at = me * per, before = from.before;
-        int seq = from.seq, spans = 0, first_item = 0, first_seq = 0;
+        const int end = min(from.rounds * items, (me + 1) * per); // in rounds of items
+        int at = me * per, before = from.before, seq = from.seq, len = from.len;
+        int spans = 0, first_item = 0, first_seq = 0;
         while (at < end && seq < a.seqs) {
-            const int len = __builtin_amdgcn_readfirstlane(clampi(a.lens[seq], 0, a.longest));
-            const int r = rounds_of(len, kRound);
+            const int r = rounds_of(len, round);
             if (r > 0) {
-                const int64_t in = at - before * items;
-                const int item = __builtin_amdgcn_readfirstlane((int)(in / r));
-                const int off = __builtin_amdgcn_readfirstlane((int)(in - (int64_t)item * r));
-                const int take = __builtin_amdgcn_readfirstlane((int)min((int64_t)(r - off), end - at));
+                const int in = at - before * items, item = in / r, off = in - item * r, take = min(r - off, end - at);
                 const bool begins = off == 0, ends = off + take == r;
-                attend(seq, item, off * kRound, min(len, (off + take) * kRound), begins && ends ? -1 : 2 * me + begins);
+                attend(seq, __builtin_amdgcn_readfirstlane(item), __builtin_amdgcn_readfirstlane(off * round),
+                       __builtin_amdgcn_readfirstlane(min(len, (off + take) * round)), begins && ends ? -1 : 2 * me + begins);
                 if (begins && !ends) { // this share and those up to the item's last round
-                    spans = (int)((at + r - 1) / per) - me + 1;
+                    spans = (at + r - 1) / per - me + 1;
                     first_seq = seq;
                     first_item = item;
                 }
                 at += take;
-                if (item + 1 < items || !ends) {
-                    __syncthreads(); // the join has read the V buffers
+                __syncthreads(); // the join has read the V buffers
+                if (item + 1 < items || !ends)
                     continue;
-                }
             }
             before += r;
-            ++seq;
-            __syncthreads();
+            if (++seq < a.seqs)
+                len = __builtin_amdgcn_readfirstlane(clampi(a.lens[seq], 0, a.longest));
         }
         if (threadIdx.x == 0) {
             a.spans[3 * me] = spans;
@@ -452,18 +452,26 @@ template <int D, bool F16> hipError_t run_d(const DecodeArgs &a, const DecodePla
 // stages).
 // Equal shares cost a look for the share's start, a bubble at each item's end
 // and the join.  A workgroup per item is quicker where an item is two tiles a
-// wave at most (one sequence, 8 heads: 8.0 us for 512 tokens, and 11.4 for 513
-// in shares; past that each tile a wave adds 2.5 us), and for caches of up to 1024 keys where the items fill the device
+// wave at most (one sequence, 8 heads: 7.7 us for 512 tokens, and 9.4 for 513
+// in shares; past that each tile a wave adds 2.1 us), and for caches of up to 1024 keys where the items fill the device
 // twice (100 sequences of up to 1000 tokens, 8 heads: 52 us, and 60); there the
 // longest item, alone at the end, takes no more than some 20 us.
+// A compute unit reads at some 70 GB/s, so where a round of all waves' tiles
+// leaves more than half of the shares empty, rounds are of fewer waves (one
+// sequence of 1024 tokens, 8 heads: 9.3 us, and 10.8 in rounds of 8).
 DecodePlan plan_decode(int64_t seqs, int64_t hkv, int64_t G, int64_t longest, int cus)
 {
     DecodePlan p;
     const int64_t tiles = (G + 15) / 16;
     p.groups = (tiles + 2) / 3;
     p.nt = (tiles + p.groups - 1) / p.groups;
-    const bool direct = longest <= 512 || (longest <= 1024 && seqs * hkv * p.groups >= 2 * cus);
+    const int64_t items = seqs * hkv * p.groups;
+    const bool direct = longest <= 512 || (longest <= 1024 && items >= 2 * cus) ||
+                        items * (longest / (kWaves * kTile) + 1) >= (int64_t(1) << 30) - cus; // rounds are counted in 32 bits
     p.shares = direct ? 0 : cus;
+    p.waves = kWaves;
+    while (p.waves > 2 && 2 * items * ((longest + kTile * p.waves - 1) / (kTile * p.waves)) <= cus)
+        p.waves /= 2;
     return p;
 }
 

@@ -250,7 +250,7 @@ int tf_attn_decode(int type, const uint16_t *q, int64_t q_token, int64_t q_head,
     a.seqs = (int)seqs;
     a.G = (int)(Hq / Hkv);
     a.groups = (int)p.groups;
-    a.waves = (int)p.waves;
+    a.unit_shift = (int)p.unit_shift;
     a.longest = (int)std::min<int64_t>(longest, width * page);
     a.scale_log2 = scale * kLog2E;
     return tf::launch_attn_decode(a, (int)D, type == TF_TYPE_F16, p, static_cast<hipStream_t>(stream)) == hipSuccess

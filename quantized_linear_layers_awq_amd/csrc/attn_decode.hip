@@ -18,14 +18,16 @@
 //  - The waves' (m, l, O) are joined in LDS in wave order.
 //  - Short caches: a workgroup per (sequence, key-value head, group of 16 NT
 //    query heads), which writes the output.  Long ones: the keys of all
-//    (sequence, head, group) items, counted in rounds of 8 tiles, are laid end
-//    to end and cut into equal shares, one per workgroup and compute unit,
+//    (sequence, head, group) items, in units of a few tiles, are laid end to
+//    end and cut into equal shares, one per workgroup and compute unit,
 //    so that ragged lengths leave no tail.  A workgroup finds its share from
 //    a prefix sum of the lengths.  Items that lie whole in a share are
 //    written; the others' fp32 partials are added by attn_join_kernel in
-//    order.  No atomics.
+//    order.  No atomics.  The next item's first tile is on its way while an
+//    item's waves are joined (73 sequences of up to 1827, 12 heads of 64: 49
+//    us, and 59 without).
 // Measured, with the reading rate of a plain stream at 7.0 TB/s: 16 contexts of
-// up to 32768 tokens, 8 heads of 128 channels, 173 us (6.5 TB/s); one of 131072
+// up to 32768 tokens, 8 heads of 128 channels, 171 us (6.6 TB/s); one of 131072
 // 88 us (6.1: the kernel alone runs at 6.5, the join takes 5 us); 48 ragged ones
 // of up to 4096, 4 heads, 47 us (5.1); one of 333 tokens 6.3 us, which is the
 // latency of the chain length, pages, keys, join.
@@ -51,19 +53,19 @@ template <int D> struct Stage {
 
 template <int D> constexpr int v_swz(int row) { return D == 128 ? 2 * (row & 7) : 2 * ((row >> 1) & 3); }
 
-// Where a workgroup's share begins: the sequence, its length, and the rounds of
-// the sequences before it (one item each; the launch keeps the rounds of all
-// items below 2^31).
+// Where a workgroup's share begins: the sequence, its length, and the units of
+// the sequences before it (of one item each; a unit is 2^unit_shift keys, and the
+// launch keeps the units of all items below 2^31).
 struct Start {
-    int rounds; // of all sequences
+    int units; // of all sequences
     int before, seq, len;
 };
 
-__device__ __forceinline__ int rounds_of(int len, int round) { return (len + round - 1) / round; }
+__device__ __forceinline__ int units_of(const DecodeArgs &a, int len) { return (len + (1 << a.unit_shift) - 1) >> a.unit_shift; }
 
-// Finds rounds, and the sequence that holds round unit(rounds) of them (none
-// past the end: seq = seqs).  Every thread takes a strip of sequences.
-template <int THREADS, typename Unit> __device__ __forceinline__ Start find_start(const DecodeArgs &a, int round, Unit unit)
+// Finds units, and the sequence that holds unit place(units) of them (none past
+// the end: seq = seqs).  Every thread takes a strip of sequences.
+template <int THREADS, typename Place> __device__ __forceinline__ Start find_start(const DecodeArgs &a, Place place)
 {
     __shared__ int s_sum[THREADS / 64], s_found[3];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
@@ -72,7 +74,7 @@ template <int THREADS, typename Unit> __device__ __forceinline__ Start find_star
     int sum = 0, len = 0;
     for (int s = first; s < end; ++s) {
         len = clampi(a.lens[s], 0, a.longest);
-        sum += rounds_of(len, round);
+        sum += units_of(a, len);
     }
     int in = sum;
 #pragma unroll
@@ -92,13 +94,13 @@ template <int THREADS, typename Unit> __device__ __forceinline__ Start find_star
         before += w < wave ? x : 0;
         all += x;
     }
-    const int at = unit(all);
+    const int at = place(all);
     if (before <= at && at < before + sum) {
         int s = first;
         if (strip > 1) // the strip's sequence that holds it
             for (;; ++s) {
                 len = clampi(a.lens[s], 0, a.longest);
-                const int r = rounds_of(len, round);
+                const int r = units_of(a, len);
                 if (at < before + r)
                     break;
                 before += r;
@@ -121,7 +123,6 @@ template <int D, bool F16, int NT, bool SHARES> __global__ __launch_bounds__(64 
     constexpr int kChunks = D / 8;   // 16-byte units of a row
     constexpr int kRowsPerLoad = 1024 / kRow;
     constexpr int kWaveBytes = kTile * kRow; // V of a tile; in the join, 16 heads of D floats
-    const int waves = SHARES ? a.waves : kWaves, round = waves * kTile; // keys of a round
     static_assert(kWaveBytes == 16 * D * 4, "the join reuses the V buffers");
     __shared__ __attribute__((aligned(16))) uint8_t lds[kWaves * kWaveBytes];
     __shared__ float s_m[kWaves][16], s_l[kWaves][16];
@@ -142,146 +143,118 @@ template <int D, bool F16, int NT, bool SHARES> __global__ __launch_bounds__(64 
     const u32x4 ones = F16 ? u32x4{0x3C003C00u, 0x3C003C00u, 0x3C003C00u, 0x3C003C00u}
                            : u32x4{0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u};
 
-    // Keys c0 .. c1 - 1 of an item; the result goes to the output (slot < 0)
-    // or to a slot of the partial results.
-    auto attend = [&](int seq, int item, int c0, int c1, int slot) {
-        const int h = item % a.cache.hkv, group = item / a.cache.hkv;
-        const int tiles = (c1 - c0 + kTile - 1) / kTile;
-        const int row0 = group * 16 * NT; // first query head of the group here
+    const int page_mask = (1 << a.cache.page_shift) - 1;
+    const int64_t page_elems = (int64_t)D << a.cache.page_shift;
+    const uint32_t k_off = n * kRow + 16 * g, v_off = 16 * lane;
 
-        // Q^T operands: column n is head row0 + 16 nt + n
-        u32x4 q[NT][kSteps];
+    // Keys c0 .. c1 - 1 of an item (all uniform).  The result goes to the output
+    // (slot < 0) or to a slot of the partial results.
+    struct Segment {
+        int seq, item, c0, c1, slot;
+    };
+    // this wave's tiles of a segment: wave, wave + 8, ...
+    auto tiles_here = [&](const Segment &e) {
+        const int tiles = (e.c1 - e.c0 + kTile - 1) / kTile;
+        return tiles > wave ? (tiles - wave + kWaves - 1) / kWaves : 0;
+    };
+    // lane L: the page of 16-key run L % 2 of this wave's tile it0 + L / 2.  The
+    // load does not wait for the length (c1), which may still be on its way.
+    auto page_ids = [&](const Segment &e, int it0) {
+        const int key = e.c0 + kTile * (wave + kWaves * (it0 + (lane >> 1))) + 16 * (lane & 1);
+        int id = -1;
+        if (key < a.longest)
+            id = a.cache.tables[(int64_t)e.seq * a.cache.width + (key >> a.cache.page_shift)];
+        return key < e.c1 && id < a.cache.pages ? id : -1;
+    };
+    auto load = [&](const Segment &e, Stage<D> &st, int it, int ids) {
+        const int key0 = e.c0 + kTile * (wave + kWaves * it), h = e.item % a.cache.hkv;
+#pragma unroll
+        for (int sub = 0; sub < 2; ++sub) {
+            const int key = key0 + 16 * sub;
+            const int id = __builtin_amdgcn_readlane(ids, (2 * it + sub) & 63);
+            const int rows = id < 0 ? 0 : rows_before(e.c1, key);
+            const int64_t at = ((int64_t)max(id, 0) * a.cache.hkv + h) * page_elems + (int64_t)(key & page_mask) * D;
+            const Rsrc kr = make_rsrc_n(a.cache.k + at, rows * kRow), vr = make_rsrc_n(a.cache.v + at, rows * kRow);
+#pragma unroll
+            for (int s = 0; s < kSteps; ++s)
+                st.k[sub][s] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(kr, k_off + 64 * s, 0, kStream));
+#pragma unroll
+            for (int s = 0; s < kSteps; ++s)
+                st.v[sub][s] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(vr, v_off + 1024 * s, 0, kStream));
+        }
+    };
+    u32x4 q[NT][kSteps]; // Q^T operands: column n is head 16 NT group + 16 nt + n
+    auto load_q = [&](const Segment &e) {
+        const int h = e.item % a.cache.hkv, row0 = e.item / a.cache.hkv * 16 * NT;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             const int r = min(row0 + 16 * nt + n, a.G - 1);
-            const uint16_t *p = a.q + seq * a.q_token + (int64_t)(h * a.G + r) * a.q_head + 8 * g;
+            const uint16_t *p = a.q + e.seq * a.q_token + (int64_t)(h * a.G + r) * a.q_head + 8 * g;
 #pragma unroll
             for (int s = 0; s < kSteps; ++s)
                 q[nt][s] = load16(p + 32 * s);
         }
+    };
 
-        const int32_t *table = a.cache.tables + (int64_t)seq * a.cache.width;
-        const int page_mask = (1 << a.cache.page_shift) - 1;
-        const int64_t page_elems = (int64_t)D << a.cache.page_shift;
-
-        // lane L: the page of 16-key run L % 2 of this wave's tile it0 + L / 2
-        auto page_ids = [&](int it0) {
-            const int key = c0 + kTile * (wave + waves * (it0 + (lane >> 1))) + 16 * (lane & 1);
-            int id = -1;
-            if (key < a.longest) // not c1: the length may still be on its way
-                id = table[key >> a.cache.page_shift];
-            return key < c1 && id < a.cache.pages ? id : -1;
-        };
-        const uint32_t k_off = n * kRow + 16 * g, v_off = 16 * lane;
-        auto load = [&](Stage<D> &st, int it, int ids) {
-            const int key0 = c0 + kTile * (wave + waves * it);
+    f32x4 o[NT][kTiles], l[NT];
+    float m[NT];
+    auto compute = [&](const Segment &e, const Stage<D> &st, int it) {
 #pragma unroll
-            for (int sub = 0; sub < 2; ++sub) {
-                const int key = key0 + 16 * sub;
-                const int id = __builtin_amdgcn_readlane(ids, (2 * it + sub) & 63);
-                const int rows = id < 0 ? 0 : rows_before(c1, key);
-                const int64_t at = ((int64_t)max(id, 0) * a.cache.hkv + h) * page_elems + (int64_t)(key & page_mask) * D;
-                const Rsrc kr = make_rsrc_n(a.cache.k + at, rows * kRow), vr = make_rsrc_n(a.cache.v + at, rows * kRow);
+        for (int sub = 0; sub < 2; ++sub)
 #pragma unroll
-                for (int s = 0; s < kSteps; ++s)
-                    st.k[sub][s] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(kr, k_off + 64 * s, 0, kStream));
-#pragma unroll
-                for (int s = 0; s < kSteps; ++s)
-                    st.v[sub][s] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(vr, v_off + 1024 * s, 0, kStream));
+            for (int s = 0; s < kSteps; ++s) {
+                const int r = 16 * sub + kRowsPerLoad * s + wr_row;
+                *reinterpret_cast<u32x4 *>(vbuf + r * kRow + 16 * (wr_unit ^ v_swz<D>(r))) = st.v[sub][s];
             }
-        };
-
-        f32x4 o[NT][kTiles] = {}, l[NT] = {};
-        float m[NT];
+        const int key0 = e.c0 + kTile * (wave + kWaves * it);
+        u32x4 p[NT];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-            m[nt] = kLowest;
-        auto compute = [&](const Stage<D> &st, int it) {
+        for (int nt = 0; nt < NT; ++nt) {
+            f32x4 x[2] = {};
 #pragma unroll
             for (int sub = 0; sub < 2; ++sub)
 #pragma unroll
-                for (int s = 0; s < kSteps; ++s) {
-                    const int r = 16 * sub + kRowsPerLoad * s + wr_row;
-                    *reinterpret_cast<u32x4 *>(vbuf + r * kRow + 16 * (wr_unit ^ v_swz<D>(r))) = st.v[sub][s];
-                }
-            const int key0 = c0 + kTile * (wave + waves * it);
-            u32x4 p[NT];
+                for (int s = 0; s < kSteps; ++s)
+                    x[sub] = mfma16x16x32<F16>(st.k[sub][s], q[nt][s], x[sub]);
+            if (key0 + kTile > e.c1) {
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                f32x4 x[2] = {};
-#pragma unroll
-                for (int sub = 0; sub < 2; ++sub)
-#pragma unroll
-                    for (int s = 0; s < kSteps; ++s)
-                        x[sub] = mfma16x16x32<F16>(st.k[sub][s], q[nt][s], x[sub]);
-                if (key0 + kTile > c1) {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        if (key0 + 16 * (i >> 2) + 4 * g + (i & 3) >= c1)
-                            x[i >> 2][i & 3] = -INFINITY;
-                }
-                float top = fmaxf(fmaxf(fmaxf(x[0][0], x[0][1]), fmaxf(x[0][2], x[0][3])),
-                                  fmaxf(fmaxf(x[1][0], x[1][1]), fmaxf(x[1][2], x[1][3])));
-                top = max_swap32(max_swap16(top)) * a.scale_log2 - kHeadroom<F16>;
-                if (__builtin_amdgcn_ballot_w64(top > m[nt] + kRescaleSlack)) {
-                    const float to = fmaxf(m[nt], top), f = exp2_fast(m[nt] - to);
-                    m[nt] = to;
-                    l[nt] *= f;
-#pragma unroll
-                    for (int t = 0; t < kTiles; ++t)
-                        o[nt][t] *= f;
-                }
-                // P rounds to the inputs' type for the MFMA; the sum is taken over the
-                // rounded values (a product with ones), so that rounding cancels
-                // where a row's weight sits on few keys
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    p[nt][j] = pack_half_x2<F16>(exp2_fast(x[j >> 1][2 * (j & 1)] * a.scale_log2 - m[nt]),
-                                                 exp2_fast(x[j >> 1][2 * (j & 1) + 1] * a.scale_log2 - m[nt]));
-                l[nt] = mfma16x16x32<F16>(ones, p[nt], l[nt]);
+                for (int i = 0; i < 8; ++i)
+                    if (key0 + 16 * (i >> 2) + 4 * g + (i & 3) >= e.c1)
+                        x[i >> 2][i & 3] = -INFINITY;
             }
+            float top = fmaxf(fmaxf(fmaxf(x[0][0], x[0][1]), fmaxf(x[0][2], x[0][3])),
+                              fmaxf(fmaxf(x[1][0], x[1][1]), fmaxf(x[1][2], x[1][3])));
+            top = max_swap32(max_swap16(top)) * a.scale_log2 - kHeadroom<F16>;
+            if (__builtin_amdgcn_ballot_w64(top > m[nt] + kRescaleSlack)) {
+                const float to = fmaxf(m[nt], top), f = exp2_fast(m[nt] - to);
+                m[nt] = to;
+                l[nt] *= f;
 #pragma unroll
-            for (int t = 0; t < kTiles; ++t) {
-                const u32x2 lo = lds_read_tr(vbuf + tr[t]), hi = lds_read_tr(vbuf + tr[t] + 16 * kRow);
-                const u32x4 v = {lo[0], lo[1], hi[0], hi[1]};
+                for (int t = 0; t < kTiles; ++t)
+                    o[nt][t] *= f;
+            }
+            // P rounds to the inputs' type for the MFMA; the sum is taken over the
+            // rounded values (a product with ones), so that rounding cancels
+            // where a row's weight sits on few keys
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-                    o[nt][t] = mfma16x16x32<F16>(v, p[nt], o[nt][t]);
-            }
-        };
-
-        // this wave's tiles: wave, wave + waves, ...
-        const int mine = tiles > wave && wave < waves ? (tiles - wave + waves - 1) / waves : 0;
-        if constexpr (D == 128 && NT > 1) {
-            // more heads: the registers hold one stage beside the accumulators, and
-            // the device's other waves cover its loads
-            int ids = -1;
-            for (int it = 0; it < mine; ++it) {
-                if ((it & 31) == 0)
-                    ids = page_ids(it);
-                Stage<D> now;
-                load(now, it, ids);
-                compute(now, it);
-            }
-        } else if (mine > 0) {
-            // the loads of one stage in flight while the other is computed; a
-            // copy of the stage costs less than a second copy of the code
-            int ids = page_ids(0);
-            Stage<D> now;
-            load(now, 0, ids);
-#pragma unroll 1
-            for (int it = 0; it < mine; ++it) {
-                if (((it + 1) & 31) == 0)
-                    ids = page_ids(it + 1);
-                Stage<D> next = now;
-                if (it + 1 < mine)
-                    load(next, it + 1, ids);
-                compute(now, it);
-                now = next;
-            }
+            for (int j = 0; j < 4; ++j)
+                p[nt][j] = pack_half_x2<F16>(exp2_fast(x[j >> 1][2 * (j & 1)] * a.scale_log2 - m[nt]),
+                                             exp2_fast(x[j >> 1][2 * (j & 1) + 1] * a.scale_log2 - m[nt]));
+            l[nt] = mfma16x16x32<F16>(ones, p[nt], l[nt]);
         }
+#pragma unroll
+        for (int t = 0; t < kTiles; ++t) {
+            const u32x2 lo = lds_read_tr(vbuf + tr[t]), hi = lds_read_tr(vbuf + tr[t] + 16 * kRow);
+            const u32x4 v = {lo[0], lo[1], hi[0], hi[1]};
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+                o[nt][t] = mfma16x16x32<F16>(v, p[nt], o[nt][t]);
+        }
+    };
 
-        // join the waves, 16 heads at a time
+    // join the waves, 16 heads at a time
+    auto finish = [&](const Segment &e) {
+        const int h = e.item % a.cache.hkv, row0 = e.item / a.cache.hkv * 16 * NT;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             const int heads = min(16, a.G - row0 - 16 * nt);
@@ -291,9 +264,8 @@ template <int D, bool F16, int NT, bool SHARES> __global__ __launch_bounds__(64 
             float *const mine_o = reinterpret_cast<float *>(lds + wave * kWaveBytes);
             if (n < heads) {
 #pragma unroll
-                for (int t = 0; t < kTiles; ++t)
-                    *reinterpret_cast<f32x4 *>(mine_o + n * D + 4 * ((4 * t + g) ^ n)) = o[nt][t]; // 4-float units, XORed
-                                                                                                   // by head: no bank conflicts
+                for (int t = 0; t < kTiles; ++t) // 4-float units, XORed by head: no bank conflicts
+                    *reinterpret_cast<f32x4 *>(mine_o + n * D + 4 * ((4 * t + g) ^ n)) = o[nt][t];
                 if (g == 0) {
                     s_m[wave][n] = m[nt];
                     s_l[wave][n] = l[nt][0];
@@ -315,12 +287,12 @@ template <int D, bool F16, int NT, bool SHARES> __global__ __launch_bounds__(64 
                     x += f * p[0];
                     y += f * p[1];
                 }
-                if (slot < 0) {
-                    const int64_t at = (int64_t)seq * a.cache.hkv * a.G + h * a.G + row0 + 16 * nt + r;
+                if (e.slot < 0) {
+                    const int64_t at = (int64_t)e.seq * a.cache.hkv * a.G + h * a.G + row0 + 16 * nt + r;
                     const float inv = sum == 0.f ? 1.f : 1.f / sum;
                     *reinterpret_cast<uint32_t *>(a.out + at * D + c) = pack_half_x2<F16>(x * inv, y * inv);
                 } else {
-                    const int64_t at = (int64_t)slot * 16 * NT + 16 * nt + r;
+                    const int64_t at = (int64_t)e.slot * 16 * NT + 16 * nt + r;
                     *reinterpret_cast<f32x2 *>(a.part + at * D + c) = f32x2{x, y};
                     if (c == 0)
                         *reinterpret_cast<f32x2 *>(a.stats + 2 * at) = f32x2{top, sum};
@@ -329,45 +301,110 @@ template <int D, bool F16, int NT, bool SHARES> __global__ __launch_bounds__(64 
         }
     };
 
+    // Segments one after the other: the pages of the next one's first tiles are
+    // asked for before this one's tiles, its queries and its first tile before
+    // this one's waves are joined.  next(e, f) names the segment after e.
+    constexpr bool kTwoStages = D == 64 || NT == 1; // else the registers hold one, and the other waves cover its loads
+    auto run = [&](Segment e, auto next) {
+        Stage<D> now;
+        int ids = page_ids(e, 0), mine = tiles_here(e);
+        load_q(e);
+        if (kTwoStages && mine > 0)
+            load(e, now, 0, ids);
+        for (;;) {
+            Segment f;
+            const bool more = next(e, f);
+            const int ids_after = more ? page_ids(f, 0) : -1;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                m[nt] = kLowest;
+                l[nt] = f32x4{};
+#pragma unroll
+                for (int t = 0; t < kTiles; ++t)
+                    o[nt][t] = f32x4{};
+            }
+#pragma unroll 1
+            for (int it = 0; it < mine; ++it) {
+                if constexpr (kTwoStages) {
+                    // the loads of one stage in flight while the other is
+                    // computed; a copy of the stage costs less than a second
+                    // copy of the code
+                    if (((it + 1) & 31) == 0)
+                        ids = page_ids(e, it + 1);
+                    Stage<D> after = now;
+                    if (it + 1 < mine)
+                        load(e, after, it + 1, ids);
+                    compute(e, now, it);
+                    now = after;
+                } else {
+                    if (it && (it & 31) == 0)
+                        ids = page_ids(e, it);
+                    load(e, now, it, ids);
+                    compute(e, now, it);
+                }
+            }
+            if (more) {
+                ids = ids_after;
+                mine = tiles_here(f);
+                load_q(f);
+                if (kTwoStages && mine > 0)
+                    load(f, now, 0, ids);
+            }
+            finish(e);
+            if (!more)
+                break;
+            __syncthreads(); // the join has read the V buffers
+            e = f;
+        }
+    };
+
     if constexpr (!SHARES) {
         const int seq = blockIdx.y, len = clampi(a.lens[seq], 0, a.longest);
-        attend(seq, blockIdx.x, 0, __builtin_amdgcn_readfirstlane(len), -1);
+        run(Segment{seq, (int)blockIdx.x, 0, __builtin_amdgcn_readfirstlane(len), -1}, [](const Segment &, Segment &) { return false; });
     } else {
         const int me = blockIdx.x;
-        // sequences without keys have no rounds: their rows are zeroed here
+        // sequences without keys have no units: their rows are zeroed here
         for (int s = me; s < a.seqs; s += gridDim.x)
             if (a.lens[s] <= 0 || a.longest == 0)
                 for (int64_t u = threadIdx.x; u < (int64_t)a.cache.hkv * a.G * (D / 8); u += 64 * kWaves)
                     reinterpret_cast<u32x4 *>(a.out)[(int64_t)s * a.cache.hkv * a.G * (D / 8) + u] = u32x4{};
         int per = 0;
-        const Start from = find_start<64 * kWaves>(a, round, [&](int all) {
+        const Start from = find_start<64 * kWaves>(a, [&](int all) {
             per = (all * items + (int)gridDim.x - 1) / (int)gridDim.x;
             return me * per / items;
         });
-        const int end = min(from.rounds * items, (me + 1) * per); // in rounds of items
+        const int end = min(from.units * items, (me + 1) * per); // in units of items
         int at = me * per, before = from.before, seq = from.seq, len = from.len;
         int spans = 0, first_item = 0, first_seq = 0;
-        while (at < end && seq < a.seqs) {
-            const int r = rounds_of(len, round);
-            if (r > 0) {
-                const int in = at - before * items, item = in / r, off = in - item * r, take = min(r - off, end - at);
-                const bool begins = off == 0, ends = off + take == r;
-                attend(seq, __builtin_amdgcn_readfirstlane(item), __builtin_amdgcn_readfirstlane(off * round),
-                       __builtin_amdgcn_readfirstlane(min(len, (off + take) * round)), begins && ends ? -1 : 2 * me + begins);
-                if (begins && !ends) { // this share and those up to the item's last round
-                    spans = (at + r - 1) / per - me + 1;
-                    first_seq = seq;
-                    first_item = item;
+        // the segment that begins at `at`, and the place after it
+        auto take = [&](Segment &e) {
+            while (at < end && seq < a.seqs) {
+                const int r = units_of(a, len), in = at - before * items;
+                if (in < r * items) {
+                    const int item = in / r, off = in - item * r, n_units = min(r - off, end - at);
+                    const bool begins = off == 0, ends = off + n_units == r;
+                    e.seq = seq;
+                    e.item = __builtin_amdgcn_readfirstlane(item);
+                    e.c0 = __builtin_amdgcn_readfirstlane(off << a.unit_shift);
+                    e.c1 = __builtin_amdgcn_readfirstlane(min(len, (off + n_units) << a.unit_shift));
+                    e.slot = begins && ends ? -1 : 2 * me + begins;
+                    if (begins && !ends) { // this share and those up to the item's last unit
+                        spans = (at + r - 1) / per - me + 1;
+                        first_seq = seq;
+                        first_item = item;
+                    }
+                    at += n_units;
+                    return true;
                 }
-                at += take;
-                __syncthreads(); // the join has read the V buffers
-                if (item + 1 < items || !ends)
-                    continue;
+                before += r;
+                if (++seq < a.seqs)
+                    len = __builtin_amdgcn_readfirstlane(clampi(a.lens[seq], 0, a.longest));
             }
-            before += r;
-            if (++seq < a.seqs)
-                len = __builtin_amdgcn_readfirstlane(clampi(a.lens[seq], 0, a.longest));
-        }
+            return false;
+        };
+        Segment first;
+        if (take(first))
+            run(first, [&](const Segment &, Segment &f) { return take(f); });
         if (threadIdx.x == 0) {
             a.spans[3 * me] = spans;
             a.spans[3 * me + 1] = first_seq;
@@ -450,15 +487,19 @@ template <int D, bool F16> hipError_t run_d(const DecodeArgs &a, const DecodePla
 // Query heads of a key-value head are covered by groups of nt tiles of 16, at
 // most three (the accumulators of more do not fit the registers beside two
 // stages).
-// Equal shares cost a look for the share's start, a bubble at each item's end
-// and the join.  A workgroup per item is quicker where an item is two tiles a
-// wave at most (one sequence, 8 heads: 7.7 us for 512 tokens, and 9.4 for 513
-// in shares; past that each tile a wave adds 2.1 us), and for caches of up to 1024 keys where the items fill the device
-// twice (100 sequences of up to 1000 tokens, 8 heads: 52 us, and 60); there the
-// longest item, alone at the end, takes no more than some 20 us.
-// A compute unit reads at some 70 GB/s, so where a round of all waves' tiles
-// leaves more than half of the shares empty, rounds are of fewer waves (one
-// sequence of 1024 tokens, 8 heads: 9.3 us, and 10.8 in rounds of 8).
+// Equal shares cost a look for the share's start and the join.  A workgroup per
+// item is quicker where an item is two tiles a wave at most (one sequence, 8
+// heads: 7.7 us for 512 tokens, and 8.8 for 513 in shares; past that each tile a
+// wave adds 2.1 us), and for caches of up to 1024 keys where the items fill the
+// device twice (100 sequences of up to 1000 tokens, 8 heads: 52 us, and 60);
+// there the longest item, alone at the end, takes no more than some 20 us.
+// Shares are cut at whole units: 8 tiles, one for each wave, where there are many
+// items, so that the items of a sequence are cut at the same pages, which
+// neighbouring workgroups then read together (20 sequences of up to 3000, 32
+// heads: 83 us, and 126 in units of one tile); fewer where an item is spread over
+// more than sixteen shares and a unit of 8 would leave shares empty or unequal (one
+// sequence of 2048 tokens, 8 heads: 9.7 us in units of 2, 11.6 of 8; of 17911:
+// 21.2 in units of 4, 23.0 of 8).
 DecodePlan plan_decode(int64_t seqs, int64_t hkv, int64_t G, int64_t longest, int cus)
 {
     DecodePlan p;
@@ -467,11 +508,9 @@ DecodePlan plan_decode(int64_t seqs, int64_t hkv, int64_t G, int64_t longest, in
     p.nt = (tiles + p.groups - 1) / p.groups;
     const int64_t items = seqs * hkv * p.groups;
     const bool direct = longest <= 512 || (longest <= 1024 && items >= 2 * cus) ||
-                        items * (longest / (kWaves * kTile) + 1) >= (int64_t(1) << 30) - cus; // rounds are counted in 32 bits
+                        items * (longest / 64 + 1) >= (int64_t(1) << 30) - 2 * cus; // units are counted in 32 bits
     p.shares = direct ? 0 : cus;
-    p.waves = kWaves;
-    while (p.waves > 2 && 2 * items * ((longest + kTile * p.waves - 1) / (kTile * p.waves)) <= cus)
-        p.waves /= 2;
+    p.unit_shift = 16 * items >= cus ? 8 : items * ((longest + 63) / 64) > 2 * cus ? 7 : 6;
     return p;
 }
 

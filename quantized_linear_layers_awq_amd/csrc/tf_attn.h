@@ -21,12 +21,12 @@ struct DecodeArgs {
     float *stats;   // [shares][2][16 nt][2]: their maximum and sum
     int32_t *spans; // [shares][3]: shares of the item that begins here and ends later (0: none), its sequence and number
     int seqs, G, groups, longest;
-    int waves; // of a round of tiles, when shares are equal
+    int unit_shift; // shares are cut at multiples of 2^unit_shift keys
     float scale_log2;
 };
 struct DecodePlan {
     int64_t nt, groups, shares; // shares == 0: a workgroup per item
-    int64_t waves;
+    int64_t unit_shift;
 };
 DecodePlan plan_decode(int64_t seqs, int64_t hkv, int64_t G, int64_t longest, int cus);
 hipError_t launch_attn_decode(const DecodeArgs &a, int D, bool f16, const DecodePlan &p, hipStream_t st);

@@ -7,7 +7,7 @@
 // What bounds it: the cache is read once, 4 D bytes per token and key-value
 // head against 4 G D operations, so HBM does.  The kernel is a stream of
 // key tiles with the arithmetic hidden under it:
-//  - A workgroup's 8 waves each take every eighth 32-key tile of its range on
+//  - A workgroup's W waves each take every W-th 32-key tile of its range on
 //    their own: K goes from memory straight into MFMA operand registers, V
 //    through the wave's own LDS buffer (row-major in, transposed out), the
 //    next tile's loads in flight meanwhile.  No barrier before the end.
@@ -37,7 +37,6 @@ namespace tf {
 
 namespace {
 
-constexpr int kWaves = 8;
 constexpr int kTile = 32;
 // Cache policy of the keys and values: streamed (nt), for they are read once a
 // step and the next layer's displace them.  Against the default, four caches
@@ -114,8 +113,8 @@ template <int THREADS, typename Place> __device__ __forceinline__ Start find_sta
             __builtin_amdgcn_readfirstlane(s_found[2])};
 }
 
-// SHARES: equal shares of all keys, else one item of one sequence
-template <int D, bool F16, int NT, bool SHARES> __global__ __launch_bounds__(64 * kWaves, 2) void attn_decode_kernel(DecodeArgs a)
+// W waves; SHARES: equal shares of all keys, else one item of one sequence
+template <int D, bool F16, int NT, int W, bool SHARES> __global__ __launch_bounds__(64 * W, 2) void attn_decode_kernel(DecodeArgs a)
 {
     constexpr int kSteps = D / 32;   // MFMA steps over channels
     constexpr int kTiles = D / 16;   // 16-channel tiles of O^T
@@ -124,8 +123,8 @@ template <int D, bool F16, int NT, bool SHARES> __global__ __launch_bounds__(64 
     constexpr int kRowsPerLoad = 1024 / kRow;
     constexpr int kWaveBytes = kTile * kRow; // V of a tile; in the join, 16 heads of D floats
     static_assert(kWaveBytes == 16 * D * 4, "the join reuses the V buffers");
-    __shared__ __attribute__((aligned(16))) uint8_t lds[kWaves * kWaveBytes];
-    __shared__ float s_m[kWaves][16], s_l[kWaves][16];
+    __shared__ __attribute__((aligned(16))) uint8_t lds[W * kWaveBytes];
+    __shared__ float s_m[W][16], s_l[W][16];
 
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int g = lane >> 4, n = lane & 15;
@@ -152,22 +151,22 @@ template <int D, bool F16, int NT, bool SHARES> __global__ __launch_bounds__(64 
     struct Segment {
         int seq, item, c0, c1, slot;
     };
-    // this wave's tiles of a segment: wave, wave + 8, ...
+    // this wave's tiles of a segment: wave, wave + W, ...
     auto tiles_here = [&](const Segment &e) {
         const int tiles = (e.c1 - e.c0 + kTile - 1) / kTile;
-        return tiles > wave ? (tiles - wave + kWaves - 1) / kWaves : 0;
+        return tiles > wave ? (tiles - wave + W - 1) / W : 0;
     };
     // lane L: the page of 16-key run L % 2 of this wave's tile it0 + L / 2.  The
     // load does not wait for the length (c1), which may still be on its way.
     auto page_ids = [&](const Segment &e, int it0) {
-        const int key = e.c0 + kTile * (wave + kWaves * (it0 + (lane >> 1))) + 16 * (lane & 1);
+        const int key = e.c0 + kTile * (wave + W * (it0 + (lane >> 1))) + 16 * (lane & 1);
         int id = -1;
         if (key < a.longest)
             id = a.cache.tables[(int64_t)e.seq * a.cache.width + (key >> a.cache.page_shift)];
         return key < e.c1 && id < a.cache.pages ? id : -1;
     };
     auto load = [&](const Segment &e, Stage<D> &st, int it, int ids) {
-        const int key0 = e.c0 + kTile * (wave + kWaves * it), h = e.item % a.cache.hkv;
+        const int key0 = e.c0 + kTile * (wave + W * it), h = e.item % a.cache.hkv;
 #pragma unroll
         for (int sub = 0; sub < 2; ++sub) {
             const int key = key0 + 16 * sub;
@@ -206,7 +205,7 @@ template <int D, bool F16, int NT, bool SHARES> __global__ __launch_bounds__(64 
                 const int r = 16 * sub + kRowsPerLoad * s + wr_row;
                 *reinterpret_cast<u32x4 *>(vbuf + r * kRow + 16 * (wr_unit ^ v_swz<D>(r))) = st.v[sub][s];
             }
-        const int key0 = e.c0 + kTile * (wave + kWaves * it);
+        const int key0 = e.c0 + kTile * (wave + W * it);
         u32x4 p[NT];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
@@ -272,15 +271,15 @@ template <int D, bool F16, int NT, bool SHARES> __global__ __launch_bounds__(64 
                 }
             }
             __syncthreads();
-            for (int u = threadIdx.x; u < heads * (D / 2); u += 64 * kWaves) {
+            for (int u = threadIdx.x; u < heads * (D / 2); u += 64 * W) {
                 const int r = u / (D / 2), c = 2 * (u % (D / 2));
                 float top = s_m[0][r];
 #pragma unroll
-                for (int w = 1; w < kWaves; ++w)
+                for (int w = 1; w < W; ++w)
                     top = fmaxf(top, s_m[w][r]);
                 float sum = 0.f, x = 0.f, y = 0.f;
 #pragma unroll
-                for (int w = 0; w < kWaves; ++w) {
+                for (int w = 0; w < W; ++w) {
                     const float f = exp2_fast(s_m[w][r] - top);
                     const float *const p = reinterpret_cast<const float *>(lds + w * kWaveBytes) + r * D + 4 * ((c >> 2) ^ r) + (c & 3);
                     sum += f * s_l[w][r];
@@ -366,10 +365,10 @@ template <int D, bool F16, int NT, bool SHARES> __global__ __launch_bounds__(64 
         // sequences without keys have no units: their rows are zeroed here
         for (int s = me; s < a.seqs; s += gridDim.x)
             if (a.lens[s] <= 0 || a.longest == 0)
-                for (int64_t u = threadIdx.x; u < (int64_t)a.cache.hkv * a.G * (D / 8); u += 64 * kWaves)
+                for (int64_t u = threadIdx.x; u < (int64_t)a.cache.hkv * a.G * (D / 8); u += 64 * W)
                     reinterpret_cast<u32x4 *>(a.out)[(int64_t)s * a.cache.hkv * a.G * (D / 8) + u] = u32x4{};
         int per = 0;
-        const Start from = find_start<64 * kWaves>(a, [&](int all) {
+        const Start from = find_start<64 * W>(a, [&](int all) {
             per = (all * items + (int)gridDim.x - 1) / (int)gridDim.x;
             return me * per / items;
         });
@@ -467,10 +466,14 @@ template <int D, bool F16, int NT> __global__ __launch_bounds__(256) void attn_j
 template <int D, bool F16, int NT> hipError_t run(const DecodeArgs &a, const DecodePlan &p, hipStream_t st)
 {
     if (p.shares == 0) {
-        attn_decode_kernel<D, F16, NT, false><<<dim3(a.cache.hkv * a.groups, a.seqs), 64 * kWaves, 0, st>>>(a);
+        const dim3 grid(a.cache.hkv * a.groups, a.seqs);
+        if (p.waves == 2)
+            attn_decode_kernel<D, F16, NT, 2, false><<<grid, 128, 0, st>>>(a);
+        else
+            attn_decode_kernel<D, F16, NT, 8, false><<<grid, 512, 0, st>>>(a);
         return hipGetLastError();
     }
-    attn_decode_kernel<D, F16, NT, true><<<(unsigned)p.shares, 64 * kWaves, 0, st>>>(a);
+    attn_decode_kernel<D, F16, NT, 8, true><<<(unsigned)p.shares, 512, 0, st>>>(a);
     if (hipError_t e = hipGetLastError(); e != hipSuccess)
         return e;
     attn_join_kernel<D, F16, NT><<<dim3((unsigned)p.shares, std::min(a.G, 16 * NT)), 256, 0, st>>>(a);
@@ -493,6 +496,10 @@ template <int D, bool F16> hipError_t run_d(const DecodeArgs &a, const DecodePla
 // wave adds 2.1 us), and for caches of up to 1024 keys where the items fill the
 // device twice (100 sequences of up to 1000 tokens, 8 heads: 52 us, and 60);
 // there the longest item, alone at the end, takes no more than some 20 us.
+// Workgroups per item have two waves, of which four fit a compute unit, where
+// there are many of them or few keys (128 sequences of up to 200, 8 heads: 14.2
+// us, and 20.6 with eight waves; one of 64: 3.3 us, and 3.7), else eight (one of
+// 333: 6.4 us, and 7.0 with two).
 // Shares are cut at whole units: 8 tiles, one for each wave, where there are many
 // items, so that the items of a sequence are cut at the same pages, which
 // neighbouring workgroups then read together (20 sequences of up to 3000, 32
@@ -510,6 +517,7 @@ DecodePlan plan_decode(int64_t seqs, int64_t hkv, int64_t G, int64_t longest, in
     const bool direct = longest <= 512 || (longest <= 1024 && items >= 2 * cus) ||
                         items * (longest / 64 + 1) >= (int64_t(1) << 30) - 2 * cus; // units are counted in 32 bits
     p.shares = direct ? 0 : cus;
+    p.waves = longest <= 128 || items >= 2 * cus ? 2 : 8;
     p.unit_shift = 16 * items >= cus ? 8 : items * ((longest + 63) / 64) > 2 * cus ? 7 : 6;
     return p;
 }

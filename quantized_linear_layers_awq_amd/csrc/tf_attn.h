@@ -26,7 +26,7 @@ struct DecodeArgs {
 };
 struct DecodePlan {
     int64_t nt, groups, shares; // shares == 0: a workgroup per item
-    int64_t unit_shift;
+    int64_t waves, unit_shift;  // of a workgroup per item; of shares
 };
 DecodePlan plan_decode(int64_t seqs, int64_t hkv, int64_t G, int64_t longest, int cus);
 hipError_t launch_attn_decode(const DecodeArgs &a, int D, bool f16, const DecodePlan &p, hipStream_t st);

@@ -494,7 +494,7 @@ template <int D, bool F16> hipError_t run_d(const DecodeArgs &a, const DecodePla
 // item is quicker where an item is two tiles a wave at most (one sequence, 8
 // heads: 7.7 us for 512 tokens, and 8.8 for 513 in shares; past that each tile a
 // wave adds 2.1 us), and for caches of up to 1024 keys where the items fill the
-// device twice (100 sequences of up to 1000 tokens, 8 heads: 52 us, and 60);
+// device twice (128 sequences of up to 900 tokens, 4 heads: 32 us, and 40);
 // there the longest item, alone at the end, takes no more than some 20 us.
 // Workgroups per item have two waves, of which four fit a compute unit, where
 // there are many of them or few keys (128 sequences of up to 200, 8 heads: 14.2
@@ -517,7 +517,7 @@ DecodePlan plan_decode(int64_t seqs, int64_t hkv, int64_t G, int64_t longest, in
     const bool direct = longest <= 512 || (longest <= 1024 && items >= 2 * cus) ||
                         items * (longest / 64 + 1) >= (int64_t(1) << 30) - 2 * cus; // units are counted in 32 bits
     p.shares = direct ? 0 : cus;
-    p.waves = longest <= 128 || items >= 2 * cus ? 2 : 8;
+    p.waves = longest <= 128 || items > cus ? 2 : 8;
     p.unit_shift = 16 * items >= cus ? 8 : items * ((longest + 63) / 64) > 2 * cus ? 7 : 6;
     return p;
 }

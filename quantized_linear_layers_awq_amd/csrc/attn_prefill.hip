@@ -28,13 +28,15 @@
 //  - Wave w copies rows 16 w .. 16 w + 15, which lie in one page (pages hold a
 //    multiple of 16 tokens): one page id per wave and tile.
 //  - Workgroups that run side by side share keys and values in their XCD's L2:
-//    they are ordered by bundles of sequences and heads that fit there, and in
-//    a bundle with the last rows first, which see the most keys (four
-//    sequences of up to 6000 tokens, 64/8 heads: 601 us, and 1029 with all
-//    four side by side).
+//    sequences and groups of heads follow one another where not all of them fit
+//    (four sequences of up to 6000 tokens, 64/8 heads: 601 us, and 1029 side by
+//    side); where they do, all run side by side, the blocks that see the most
+//    keys first, and no workgroup starts for a block that a shorter sequence
+//    does not have (7 prompts of up to 1553, 32/8 heads: 120 us, and 142 with
+//    those).
 //  - Few rows behind many keys: the keys are cut into ranges and joined.
-// Measured: one prompt of 8192 tokens, 32/8 heads of 128, 500 to 513 us (1070
-// to 1100 TFLOP/s; a library product of 8192 x 8192 matrices runs at 1116, of
+// Measured: one prompt of 8192 tokens, 32/8 heads of 128, 494 to 525 us by the
+// board (1050 to 1110 TFLOP/s; a library product of 8192 x 8192 matrices runs at 1116, of
 // 16384 at 1348), MFMAs busy 55 % of 1.87 GHz.  Without the exponentials, the
 // maximum and the sum the same loop takes 480: the matrix units and the power
 // they draw bound it.  For 64 channels, with as many exponentials for half the
@@ -49,6 +51,7 @@ constexpr int kWaves = 4;
 constexpr int kKeys = 64;
 constexpr int kMinRange = 4;   // tiles of a range of keys, at least
 constexpr int kMaxSplits = 16; // ranges
+constexpr int64_t kSlots = 512; // workgroups that run at a time
 constexpr int64_t kL2Share = 3 << 20; // bytes of an XCD's 4 MiB for the keys and values in use
 
 // tiles of a range when the keys of a sequence are cut into `splits`
@@ -89,15 +92,46 @@ template <int D, bool F16, bool PAGED> __global__ __launch_bounds__(64 * kWaves,
 
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int half = lane >> 5, n = lane & 31;
-    // bundle of sequences, group of heads, block of rows, sequence in the
-    // bundle, head in the group (fastest)
-    const int pairs = a.seqs_by * a.heads_by, groups = a.hkv / a.heads_by;
-    const int bundle = blockIdx.x / (a.blocks * pairs), rest = blockIdx.x % (a.blocks * pairs);
-    const int block = a.blocks - 1 - rest / pairs, pair = rest % pairs;
-    const int seq = bundle / groups * a.seqs_by + pair / a.heads_by;
-    const int h = bundle % groups * a.heads_by + pair % a.heads_by;
-    if (seq >= a.seqs)
-        return;
+    int seq, h, block;
+    if (a.all_blocks) {
+        // only the blocks that there are, last ones first, each level's
+        // sequences side by side: lane s holds the number of sequence s
+        const int turn = blockIdx.x / a.hkv;
+        h = blockIdx.x % a.hkv;
+        int mine = 0;
+        if (lane < a.seqs) {
+            const int from = clampi(a.cu_q[lane], 0, a.tokens), to = clampi(a.cu_q[lane + 1], 0, a.tokens);
+            mine = (int)(((int64_t)clampi(to - from, 0, a.longest) * a.G + kPrefillRows - 1) / kPrefillRows);
+        }
+        // blocks at level b (lane's own b) and above
+        auto from_level = [&](int b) {
+            int sum = 0;
+            for (int s = 0; s < a.seqs; ++s)
+                sum += max(__builtin_amdgcn_readlane(mine, s) - b, 0);
+            return sum;
+        };
+        // the highest level that counts more than `turn` blocks from it on,
+        // 64 levels at a time
+        int low = 0;
+        for (int step = a.steps; step > 0; step >>= 6) {
+            const uint64_t past = __builtin_amdgcn_ballot_w64(from_level(low + step * lane) > turn);
+            if (past == 0)
+                return; // no such block
+            low += step * (63 - __builtin_clzll(past));
+        }
+        block = low;
+        const int rank = turn - __builtin_amdgcn_readfirstlane(from_level(block + 1)); // among the level's sequences
+        const uint64_t there = __builtin_amdgcn_ballot_w64(mine > block);
+        const int before = __builtin_amdgcn_mbcnt_hi((uint32_t)(there >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)there, 0));
+        seq = __builtin_ctzll(__builtin_amdgcn_ballot_w64(mine > block && before == rank));
+    } else {
+        // sequence, group of heads, block of rows (last ones first), head (fastest)
+        const int groups = a.hkv / a.heads_by, each = a.blocks * a.heads_by;
+        const int rest = blockIdx.x % each, group = blockIdx.x / each;
+        seq = group / groups;
+        h = group % groups * a.heads_by + rest % a.heads_by;
+        block = a.blocks - 1 - rest / a.heads_by;
+    }
 
     const int q0 = clampi(a.cu_q[seq], 0, a.tokens);
     const int all_new = max(clampi(a.cu_q[seq + 1], 0, a.tokens) - q0, 0);
@@ -443,8 +477,7 @@ template <int D, bool F16, bool PAGED> __global__ __launch_bounds__(256) void at
 
 template <int D, bool F16, bool PAGED> hipError_t run(const PrefillArgs &a, int64_t seqs, hipStream_t st)
 {
-    const int64_t bundles = (seqs + a.seqs_by - 1) / a.seqs_by * (a.hkv / a.heads_by);
-    const dim3 grid((unsigned)(bundles * a.seqs_by * a.heads_by * a.blocks), (unsigned)a.splits);
+    const dim3 grid((unsigned)(a.hkv * (a.all_blocks ? a.all_blocks : a.blocks * seqs)), (unsigned)a.splits);
     attn_prefill_kernel<D, F16, PAGED><<<grid, 64 * kWaves, 8 * kKeys * D, st>>>(a);
     if (hipError_t e = hipGetLastError(); e != hipSuccess || a.splits == 1)
         return e;
@@ -475,22 +508,24 @@ int plan_prefill_splits(int64_t seqs, int64_t T, int64_t hkv, int64_t G, int64_t
 hipError_t launch_attn_prefill(PrefillArgs a, int D, bool f16, bool paged, int64_t seqs, hipStream_t st)
 {
     a.blocks = (int)prefill_blocks(a.longest, a.G);
-    // How many (sequence, key-value head) pairs run side by side: as many as
-    // leave their keys and values in an XCD's L2 (a sequence taken to have
-    // the mean number of keys, or for pages what its table can name), at
-    // least eight heads or one sequence's.  Sequences run side by side only
-    // where the heads' number keeps each head on one XCD: otherwise the
-    // XCDs would share out the sequences, long and short ones (two sequences
-    // of 4096 and fewer tokens, 14/2 heads of 64: 78 us, and 60 in turn).
-    const int64_t keys = paged ? (int64_t)a.cache.width << a.cache.page_shift : a.keys / seqs;
-    const int64_t pairs = 8 * std::max<int64_t>(1, kL2Share / std::max<int64_t>(1, keys * 4 * D));
-    a.heads_by = (int)std::min<int64_t>(a.hkv, pairs);
+    // An XCD runs the workgroups whose number is its own modulo 8: with 8 heads
+    // those of one head.  Where the keys and values of all sequences and heads
+    // that it meets fit its L2 (a sequence taken to have the mean number of
+    // keys, or for pages what its table can name), all run side by side, the
+    // blocks with the most keys first.  Else one sequence after the other, in
+    // groups of as many heads as fit; so too where all workgroups run at once,
+    // for the search costs 0.4 us.
+    const int64_t keys = paged ? (int64_t)a.cache.width << a.cache.page_shift : (a.keys + seqs - 1) / seqs;
+    const int64_t pair = std::max<int64_t>(1, keys * 4 * D);
+    const int64_t most = std::min(seqs * a.blocks, (int64_t)a.tokens * a.G / kPrefillRows + seqs);
+    const bool side = seqs > 1 && seqs <= 64 && a.hkv * seqs * a.blocks > kSlots && seqs * (a.hkv % 8 ? a.hkv : a.hkv / 8) * pair <= kL2Share;
+    a.all_blocks = side ? (int)most : 0;
+    a.steps = 1;
+    while (64 * (int64_t)a.steps < a.blocks)
+        a.steps *= 64;
+    a.heads_by = (int)std::min<int64_t>(a.hkv, 8 * std::max<int64_t>(1, kL2Share / pair));
     while (a.hkv % a.heads_by)
         --a.heads_by;
-    const bool side = a.heads_by == a.hkv && a.hkv % 8 == 0;
-    const int64_t by = side ? std::max<int64_t>(1, std::min<int64_t>(pairs / a.hkv, seqs)) : 1;
-    const int64_t bundles = (seqs + by - 1) / by;
-    a.seqs_by = (int)((seqs + bundles - 1) / bundles);
     if (D == 64)
         return paged ? f16 ? run<64, true, true>(a, seqs, st) : run<64, false, true>(a, seqs, st)
                : f16 ? run<64, true, false>(a, seqs, st)

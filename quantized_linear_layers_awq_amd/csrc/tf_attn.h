@@ -45,8 +45,10 @@ struct PrefillArgs {
     int seqs, splits; // ranges of keys
     float *part;      // [T][Hq][splits][D], when splits > 1
     float *stats;     // [T][Hq][splits][2]: maximum, sum
-    // set by the launch: row blocks of a (sequence, head), and how many heads and sequences stand next to each other in the grid
-    int blocks, heads_by, seqs_by;
+    // set by the launch: row blocks of the longest (sequence, head), heads next to
+    // each other in the grid; or, all sequences side by side, no more blocks of
+    // a head than all_blocks, and the first step of the search for one
+    int blocks, heads_by, all_blocks, steps;
 };
 constexpr int kPrefillRows = 128; // rows (token, head of a group) of a workgroup
 inline int64_t prefill_blocks(int64_t longest, int64_t G) { return (longest * G + kPrefillRows - 1) / kPrefillRows; }

@@ -198,18 +198,30 @@ template <int D, bool F16, bool PAGED> __global__ __launch_bounds__(64 * kWaves,
         else
             return 0;
     };
+    // Where this wave's rows of the next tile to fetch lie (packed: tiles are
+    // fetched in order), or where this head's rows of page 0 lie (paged).
+    const uint8_t *k_next, *v_next;
+    const int64_t page_bytes = (int64_t)a.hkv * kRow << a.cache.page_shift;
+    if constexpr (PAGED) {
+        const int64_t at = ((int64_t)h << a.cache.page_shift) * kRow;
+        k_next = reinterpret_cast<const uint8_t *>(a.cache.k) + at;
+        v_next = reinterpret_cast<const uint8_t *>(a.cache.v) + at;
+    } else {
+        const int64_t key = k0 + (int64_t)kKeys * t0 + 16 * wave;
+        k_next = reinterpret_cast<const uint8_t *>(a.k + key * a.k_token + (int64_t)h * a.k_head);
+        v_next = reinterpret_cast<const uint8_t *>(a.v + key * a.v_token + (int64_t)h * a.v_head);
+    }
     auto fetch = [&](bool is_k, int t, int page) {
         const int key = kKeys * t + 16 * wave;
-        const int have = rows_before(keys, key);
-        const uint16_t *base = PAGED ? (is_k ? a.cache.k : a.cache.v) : is_k ? a.k : a.v;
+        const int have = rows_before(keys, key), stride = is_k ? kstride : vstride;
+        const uint8_t *&next = is_k ? k_next : v_next;
         Rsrc rs;
         if constexpr (PAGED) {
-            const int64_t at = (((int64_t)max(page, 0) * a.hkv + h) << a.cache.page_shift) + (key & ((1 << a.cache.page_shift) - 1));
-            rs = make_rsrc_n(base + at * D, page < 0 ? 0 : have * kRow);
+            const int64_t at = max(page, 0) * page_bytes + (key & ((1 << a.cache.page_shift) - 1)) * kRow;
+            rs = make_rsrc_n(next + at, page < 0 ? 0 : have * kRow);
         } else {
-            const int64_t at = k0 + min(key, max(keys - 1, 0));
-            rs = make_rsrc_n(base + at * (is_k ? a.k_token : a.v_token) + (int64_t)h * (is_k ? a.k_head : a.v_head),
-                             have ? (have - 1) * (is_k ? kstride : vstride) + kRow : 0);
+            rs = make_rsrc_n(next, have ? (have - 1) * stride + kRow : 0);
+            next += (int64_t)kKeys * stride;
         }
         uint8_t *const to = lds + ((is_k ? 0 : 2) + (t & 1)) * kBuf + 16 * wave * kRow;
 #pragma unroll

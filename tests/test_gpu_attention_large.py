@@ -159,3 +159,46 @@ def test_a_captured_layer_of_calls():
             assert torch.equal(a, b), f"replay {it} differs"
         # a single new token of each sequence sees every key: both calls say the same, up to the roundings of p and o
         assert bool((got[1].float() - got[2].float()).abs().max() <= 2.0**-6)
+
+
+@pytest.mark.parametrize("t", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("paged", [False, True])
+@pytest.mark.parametrize("lens,heads", [
+    # more workgroups than run at once, all sequences side by side: 75 levels of blocks, one and two steps of the search
+    ([600, 0, 17, 250, 430], (32, 2, 64)), ([512, 513, 511, 1, 0, 300], (16, 2, 64)),
+    # as many sequences as a wave has lanes, and one more, which run in turn
+    ([1 + 7 * s % 41 for s in range(64)], (64, 8, 128)), ([1 + 7 * s % 41 for s in range(65)], (64, 8, 128)),
+])
+def test_prefill_of_many_blocks(lens, heads, paged, t):
+    _, q_ = gpu_or_skip()
+    hq, hkv, d = heads
+    page = 16
+    print(f"prefill many blocks {t} paged={paged} {heads} {len(lens)} sequences", flush=True)
+    g = _gen(sum(lens) + hq)
+    cu = _starts(lens)
+    q = _normal(g, (sum(lens), hq, d), t, 1.5)
+    if paged:
+        tables, pages = ref.tables_for(lens, page, g)
+        kp, vp = (_normal(g, (pages, hkv, page, d), t) for _ in "kv")
+        out = q_.tf_attn_prefill_paged(q, kp, vp, tables.to(DEV), _ints(cu), _ints(lens), max(lens))
+
+        def keys_of(s, h):
+            return ref.gather(kp, tables[s], lens[s], h), ref.gather(vp, tables[s], lens[s], h)
+    else:
+        k, v = (_normal(g, (sum(lens), hkv, d), t) for _ in "kv")
+        out = q_.tf_attn_prefill(q, k, v, _ints(cu), _ints(cu), max(lens))
+
+        def keys_of(s, h):
+            return k[cu[s]:cu[s + 1], h].double(), v[cu[s]:cu[s + 1], h].double()
+    torch.cuda.synchronize()
+    _check_prefill(q, keys_of, cu, lens, hkv, d ** -0.5, out)
+    # a bound below the longest: its rows and no others change nothing
+    bound, given = max(lens) // 2, torch.full_like(q, 7.0)
+    if paged:
+        q_.tf_attn_prefill_paged(q, kp, vp, tables.to(DEV), _ints(cu), _ints(lens), bound, out=given)
+    else:
+        q_.tf_attn_prefill(q, k, v, _ints(cu), _ints(cu), bound, out=given)
+    torch.cuda.synchronize()
+    for s, n in enumerate(lens):
+        m = min(n, bound)
+        assert torch.equal(given[cu[s]:cu[s] + m], out[cu[s]:cu[s] + m]) and bool((given[cu[s] + m:cu[s + 1]] == 7.0).all())

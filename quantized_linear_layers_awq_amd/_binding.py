@@ -47,7 +47,10 @@ def load_library():
             return _lib
         if not os.path.exists(_LIB_PATH):
             raise ImportError(f"{_LIB_PATH} is missing: build it with quantized_linear_layers_awq_amd.build.build()")
-        L = ctypes.CDLL(_LIB_PATH)
+        # PyDLL: the GIL is held over a call.  A call of two kernels hands its
+        # partial results over in the stream's workspace, so another thread's
+        # call on the same stream must not get between them.
+        L = ctypes.PyDLL(_LIB_PATH)
         P, I64, SZ, I = ctypes.c_void_p, ctypes.c_int64, ctypes.c_size_t, ctypes.c_int
         L.tf_status_string.argtypes = [I]
         L.tf_status_string.restype = ctypes.c_char_p
@@ -196,7 +199,8 @@ def tf_repack_w8(qweight, zeros, scales, K, N, G, packed=None, stream=None):
 
 # Split-K workspaces, one per (device, stream), grown on demand.  A split
 # launch writes every partial sum it later adds up, so what a buffer holds
-# between calls does not matter; calls on one stream run in order, so one
+# between calls does not matter; calls on one stream run in order, and no
+# thread's launches get between those of another's call (load_library), so one
 # buffer per stream is never used by two calls at once.  A buffer that a
 # larger one replaces is kept, never freed: a HIP graph captured on that
 # stream still writes and reads it on every replay.

@@ -12,9 +12,10 @@
 // number: a tf_status above zero, or minus the bytes of a workspace that is
 // needed and was not given.
 //
-// The GIL is held throughout.  Some calls launch two kernels that hand over a
-// workspace, which is the stream's: two threads that call on one stream must
-// not get between them.
+// The GIL is held throughout, as it is over the linears' calls.  Some calls
+// launch two kernels that hand over a workspace, which is the stream's and which
+// the linears use too: two threads that call on one stream must not get between
+// them.
 #include <Python.h>
 
 #include <algorithm>

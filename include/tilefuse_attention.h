@@ -103,7 +103,8 @@ int tf_attn_decode(int type, const uint16_t *q, int64_t q_token, int64_t q_head,
  *   longest  an upper bound of the new tokens of a sequence (tokens past it
  *          are not computed), at most T
  *   out    [T][Hq][D]; rows of no sequence are not written
- * T and keys are at most 2^30.  The workspace holds partial results where few
+ * T and keys are at most 2^30, and seqs * Hkv * ceil(longest * (Hq / Hkv) / 128)
+ * is below 2^24 (else TF_ERR_SHAPE).  The workspace holds partial results where few
  * rows meet many keys and the keys are cut into ranges; the size depends on
  * the device's compute units, results do not depend on what it held. */
 size_t tf_attn_prefill_workspace_bytes(int64_t seqs, int64_t T, int64_t Hq, int64_t Hkv, int64_t D, int64_t longest,

@@ -14,6 +14,7 @@ constexpr int64_t kKeyLimit = int64_t(1) << 30; // key numbers, and a few tiles 
 constexpr int64_t kStrideLimit = int64_t(1) << 26; // 16 rows of a strided tensor within 31-bit byte offsets
 constexpr int64_t kGridYZ = 65535; // sequences of a decode call, a grid axis
 constexpr int kMaxGroup = 1024;
+constexpr int64_t kMaxWorkgroups = ((int64_t(1) << 32) - 1) / 256; // a launch has fewer than 2^32 threads, these kernels' workgroups 256
 
 bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
@@ -122,9 +123,9 @@ int check_prefill_sizes(int type, int64_t seqs, int64_t T, int64_t Hq, int64_t H
         return st;
     if (!count_ok(seqs, 0) || T < 0 || T > kKeyLimit || longest < 0 || longest > T || keys < 0 || keys > kKeyLimit)
         return TF_ERR_SHAPE;
-    // workgroups: at most twice the sequences' (in bundles), times the ranges of keys of a small call
+    // workgroups along the grid's first axis, at most (ranges of keys are its second)
     const int64_t blocks = std::max<int64_t>(1, tf::prefill_blocks(longest, Hq / Hkv)) * Hkv; // of a sequence: < 2^50
-    return seqs && blocks > (kIntLimit - 1) / 2 / seqs ? TF_ERR_SHAPE : TF_OK;
+    return seqs && blocks > kMaxWorkgroups / seqs ? TF_ERR_SHAPE : TF_OK;
 }
 
 // What both prefill calls ask of their queries.

@@ -1,0 +1,23 @@
+"""The largest launches of the attention and cache calls, without a GPU: a launch
+has fewer than 2^32 threads, and a call past that is refused as a shape before
+anything runs.  At the limit the arguments pass every check and end in
+TF_ERR_HIP, for no device is there."""
+
+import pytest
+
+from test_attention_host import HIP, SHAPE, call, needs_no_gpu
+
+MOST = (2**32 - 1) // 256  # workgroups of 256 threads
+
+
+@needs_no_gpu
+@pytest.mark.parametrize("name", ["tf_attn_prefill", "tf_attn_prefill_paged"])
+def test_prefill_workgroups(name):
+    # 63 blocks of 128 rows (2000 tokens, 4 heads of a group), 8 key-value heads
+    seqs = MOST // (63 * 8)
+    assert call(name, seqs=seqs) == HIP
+    assert call(name, seqs=seqs + 1) == SHAPE
+    # 256 prompts of up to 131072 tokens, 64 / 8 heads: one workgroup too many
+    many = dict(Hq=64, Hkv=8, T=1 << 20, longest=131072, q_token=64 * 128)
+    assert call(name, seqs=255, **many) == HIP
+    assert call(name, seqs=256, **many) == SHAPE

@@ -59,7 +59,8 @@ enum { TF_TYPE_BF16 = 0, TF_TYPE_F16 = 1 };
 /* D is a multiple of 16, at most 1024; page a power of two, 16 .. 1024.  A   */
 /* token whose sequence, position or page does not exist is not stored; a    */
 /* position outside the rope rows has its heads turned to zeros.  Two tokens */
-/* of one call at the same place: either's row may stay.  T == 0: TF_OK.     */
+/* of one call at the same place: either's row may stay.  T is at most        */
+/* 2^26 - 4 (else TF_ERR_SHAPE); T == 0: TF_OK.                              */
 /* ------------------------------------------------------------------------ */
 int tf_kv_append(int type, const uint16_t *qkv, int64_t qkv_token, const float *rope, int64_t rope_rows,
                  const int32_t *seq, const int32_t *pos, int64_t T, const int32_t *tables, int64_t seqs, int64_t width,

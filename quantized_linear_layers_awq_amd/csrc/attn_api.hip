@@ -171,8 +171,8 @@ int tf_kv_append(int type, const uint16_t *qkv, int64_t qkv_token, const float *
 {
     if (type != TF_TYPE_BF16 && type != TF_TYPE_F16)
         return TF_ERR_UNSUPPORTED;
-    if (!count_ok(T, 0) || Hq < 1 || Hkv < 1 || Hq >= 65536 || Hkv >= 65536 || D < 1 || !count_ok(seqs, 0) ||
-        !count_ok(rope_rows, 0) || qkv_token < (Hq + 2 * Hkv) * D)
+    if (T < 0 || T > 4 * kMaxWorkgroups || Hq < 1 || Hkv < 1 || Hq >= 65536 || Hkv >= 65536 || D < 1 || !count_ok(seqs, 0) ||
+        !count_ok(rope_rows, 0) || qkv_token < (Hq + 2 * Hkv) * D) // a workgroup has a wave for each of 4 tokens
         return TF_ERR_SHAPE;
     if (D % 16 || D > 1024)
         return TF_ERR_UNSUPPORTED;

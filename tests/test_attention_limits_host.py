@@ -21,3 +21,10 @@ def test_prefill_workgroups(name):
     many = dict(Hq=64, Hkv=8, T=1 << 20, longest=131072, q_token=64 * 128)
     assert call(name, seqs=255, **many) == HIP
     assert call(name, seqs=256, **many) == SHAPE
+
+
+@needs_no_gpu
+def test_append_workgroups():
+    # a workgroup for 4 tokens
+    assert call("tf_kv_append", T=4 * MOST) == HIP
+    assert call("tf_kv_append", T=4 * MOST + 1) == SHAPE

@@ -138,7 +138,8 @@ int tf_attn_prefill_paged(int type, const uint16_t *q, int64_t q_token, int64_t 
  *   status  int32 [1]: 0, or how many free pages were missing; then nothing is
  *           forked and the outputs equal the inputs
  * A pair with an index outside [0, seqs) is skipped.  A child is named once
- * and is no parent of the same call. */
+ * and is no parent of the same call.  (planes + 1) * forks + seqs is below
+ * 2^24 (else TF_ERR_SHAPE). */
 size_t tf_kv_fork_workspace_bytes(int64_t forks);
 int tf_kv_fork(uint16_t *cache, int64_t planes, int64_t pages, int64_t Hkv, int64_t page, int64_t D,
                const int32_t *refs, const int32_t *tables, const int32_t *lens, int64_t seqs, int64_t width,

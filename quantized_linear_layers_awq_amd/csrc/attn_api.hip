@@ -357,7 +357,9 @@ int tf_kv_fork(uint16_t *cache, int64_t planes, int64_t pages, int64_t Hkv, int6
                const int32_t *parents, const int32_t *children, int64_t forks, int32_t *refs_out, int32_t *tables_out,
                int32_t *lens_out, int32_t *status, void *workspace, size_t ws_bytes, void *stream)
 {
-    if (!count_ok(forks, 0) || (forks && planes > (kIntLimit - 1 - forks - seqs) / forks))
+    // the second launch's workgroups, counted before the first one writes
+    if (!count_ok(forks, 0) || planes < 0 || planes > 65536 || seqs < 0 || seqs > kMaxWorkgroups ||
+        (planes + 1) * forks > kMaxWorkgroups - seqs)
         return TF_ERR_SHAPE;
     if (int st = check_pool(cache, planes, pages, Hkv, page, D, refs, tables, seqs, width, refs_out, tables_out, status))
         return st;

@@ -28,3 +28,16 @@ def test_append_workgroups():
     # a workgroup for 4 tokens
     assert call("tf_kv_append", T=4 * MOST) == HIP
     assert call("tf_kv_append", T=4 * MOST + 1) == SHAPE
+
+
+@needs_no_gpu
+def test_fork_workgroups():
+    """The copies are the second of two launches: were it refused by the
+    runtime, the first would have changed the references already."""
+    big = dict(seqs=1000, ws_bytes=1 << 40)
+    forks = (MOST - 1000) // 65  # 64 planes' copies and the child's row
+    assert call("tf_kv_fork", planes=64, forks=forks, **big) == HIP
+    assert call("tf_kv_fork", planes=64, forks=forks + 1, **big) == SHAPE
+    assert call("tf_kv_fork", forks=0, seqs=MOST) == HIP
+    assert call("tf_kv_fork", forks=0, seqs=MOST + 1) == SHAPE
+    assert call("tf_kv_fork", planes=2**62, forks=2) == SHAPE

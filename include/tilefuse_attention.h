@@ -132,7 +132,8 @@ int tf_attn_prefill_paged(int type, const uint16_t *q, int64_t q_token, int64_t 
 
 /* Each children[i] becomes a copy of parents[i]: it shares the parent's full
  * pages (refs_out + 1) and gets a copy of the partial page, if there is one, in
- * the lowest free pages in the order of i.  Its table row is replaced (pages
+ * the lowest free pages in the order of i (zeros, where the entry of the partial
+ * page names none, as the parent reads it).  Its table row is replaced (pages
  * it held are not released; unused entries become -1).
  *   refs_out, tables_out, lens_out  the whole new state; may be the inputs
  *   status  int32 [1]: 0, or how many free pages were missing; then nothing is

@@ -233,11 +233,12 @@ __global__ __launch_bounds__(256) void kv_fork_kernel(PoolArgs a, int copies)
         const int i = b % a.forks;
         const int64_t plane = b / a.forks;
         const int size = plan.size[i], from = plan.from[i], to = plan.to[i];
-        if (size <= 0 || to < 0 || from < 0 || from >= a.pages)
+        if (size <= 0 || to < 0)
             return;
+        const bool there = from >= 0 && from < a.pages; // a page that does not exist reads as zeros
         const int64_t page_elems = (int64_t)a.page * a.D;
         const int units = (size % a.page) * a.D / 8; // 16-byte units of a head
-        const uint16_t *src = a.cache + (plane * a.pages + from) * a.hkv * page_elems;
+        const uint16_t *src = a.cache + (plane * a.pages + (there ? from : to)) * a.hkv * page_elems;
         uint16_t *dst = a.cache + (plane * a.pages + to) * a.hkv * page_elems;
         auto at = [&](int u) { return (u / units) * page_elems + 8 * (u % units); };
         int u = tid;
@@ -245,13 +246,13 @@ __global__ __launch_bounds__(256) void kv_fork_kernel(PoolArgs a, int copies)
             u32x4 x[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                x[i] = load16(src + at(u + 256 * i));
+                x[i] = there ? load16(src + at(u + 256 * i)) : u32x4{};
 #pragma unroll
             for (int i = 0; i < 4; ++i)
                 *reinterpret_cast<u32x4 *>(dst + at(u + 256 * i)) = x[i];
         }
         for (; u < units * a.hkv; u += 256)
-            *reinterpret_cast<u32x4 *>(dst + at(u)) = load16(src + at(u));
+            *reinterpret_cast<u32x4 *>(dst + at(u)) = there ? load16(src + at(u)) : u32x4{};
         return;
     }
     b -= copies;

@@ -145,7 +145,8 @@ class Decoder:
         return self.run(x, attend)
 
     def whole(self, x):
-        """One sequence at once, without a cache: packed keys straight from the (rotated) QKV output."""
+        """One sequence at once: append rotates its keys into scratch pages, which are gathered into packed
+        ones (the QKV output itself keeps unrotated keys)."""
         n = len(x)
         cu = ints([0, n])
         pages = -(-n // 128)

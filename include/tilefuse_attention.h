@@ -5,8 +5,11 @@
  *
  * A layer's step: the QKV linear -> tf_kv_append (rotate queries and keys,
  * write keys and values into the cache) -> tf_attn_decode (one new token per
- * sequence) or tf_attn_prefill / tf_attn_prefill_paged (many) -> the output
- * linear.  tf_kv_fork and tf_kv_compact keep the pool of pages.
+ * sequence) or tf_attn_prefill_paged (many) -> the output linear.  The rotated
+ * keys are in the pages alone: tf_kv_append leaves the QKV output as it was.
+ * tf_attn_prefill is for keys that stand packed: whose positions are encoded in
+ * another way, or that the caller has rotated.
+ * tf_kv_fork and tf_kv_compact keep the pool of pages.
  *
  * Notation: T tokens, Hq query heads, Hkv key-value heads (Hq a multiple:
  * query head j reads key-value head j / (Hq / Hkv)), D channels of a head.
@@ -99,7 +102,9 @@ int tf_attn_decode(int type, const uint16_t *q, int64_t q_token, int64_t q_head,
  * token sees every key, the one before it one fewer, and so on.
  *   q      [T][Hq][D], strides q_token, q_head
  *   k, v   [keys][Hkv][D] with strides of their own: all three may be parts of
- *          one fused QKV output
+ *          one fused QKV output.  They are taken as they are: beside queries
+ *          that tf_kv_append has rotated, the QKV output's keys, which it has
+ *          not, are the wrong ones
  *   cu_q, cu_k  int32 [seqs + 1], ascending; clamped to the tensors
  *   longest  an upper bound of the new tokens of a sequence (tokens past it
  *          are not computed), at most T

@@ -88,7 +88,10 @@ def tf_attn_prefill(q, k, v, cu_q, cu_k, longest, scale=None, out=None, workspac
     [keys][Hkv][D] (channels contiguous; parts of one fused QKV output will
     do), sequence s in rows cu_q[s] .. cu_q[s + 1] of q and cu_k[s] ..
     cu_k[s + 1] of k and v (int32 [seqs + 1]), its last token seeing every
-    key.  `longest` bounds the new tokens of a sequence.  Returns [T][Hq][D]."""
+    key.  `longest` bounds the new tokens of a sequence.  Keys are taken as they
+    are: those of a QKV output are not rotated by tf_kv_append, whose rotated
+    keys are in the pages (tf_attn_prefill_paged).  Returns [T][Hq][D]; rows of
+    no sequence and past the bound are not written."""
     return _run("tf_attn_prefill", _native().attn_prefill, q, stream, q, k, v, cu_q, cu_k, longest, scale, out, workspace)
 
 
@@ -96,7 +99,8 @@ def tf_attn_prefill_paged(q, k_pages, v_pages, tables, cu_q, lens, longest, scal
                           stream=None):
     """Causal attention of packed new tokens q [T][Hq][D] (sequence s in rows
     cu_q[s] .. cu_q[s + 1]) over the first lens[s] tokens of the sequences'
-    pages, the new ones included.  Returns [T][Hq][D]."""
+    pages, the new ones included.  Returns [T][Hq][D]; rows of no sequence and
+    past the bound (`longest` new tokens) are not written."""
     return _run("tf_attn_prefill_paged", _native().attn_prefill_paged, q, stream, q, k_pages, v_pages, tables, cu_q, lens,
                 longest, scale, out, workspace)
 

@@ -131,8 +131,8 @@ int tf_attn_prefill_paged(int type, const uint16_t *q, int64_t q_token, int64_t 
 
 /* ------------------------------------------------------------------------ */
 /* The pool.  refs int32 [pages] counts the table entries that name a page;  */
-/* 0 is a free page.  cache is [planes][pages][Hkv][page][D], any 16-bit type, */
-/* D a multiple of 8; page is 1 .. 1024.                                      */
+/* a page of 0 or less is free.  cache is [planes][pages][Hkv][page][D], any  */
+/* 16-bit type, D a multiple of 8; page is 1 .. 1024.                        */
 /* ------------------------------------------------------------------------ */
 
 /* Each children[i] becomes a copy of parents[i]: it shares the parent's full

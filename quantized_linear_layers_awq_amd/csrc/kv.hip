@@ -140,7 +140,7 @@ __device__ __forceinline__ int parent_length(const PoolArgs &a, int p)
 }
 
 // One workgroup: ranks the children that need a page (prefix sum), finds the
-// free pages of those ranks in ascending order (prefix sum over refs == 0),
+// free pages of those ranks in ascending order (prefix sum over refs <= 0),
 // copies refs.  Latency-bound; 8192 pages per step.
 __global__ __launch_bounds__(kScan) void kv_fork_plan_kernel(PoolArgs a)
 {
@@ -189,7 +189,7 @@ __global__ __launch_bounds__(kScan) void kv_fork_plan_kernel(PoolArgs a)
         int count = 0;
 #pragma unroll
         for (int j = 0; j < kCells; ++j)
-            count += r[j] == 0;
+            count += r[j] <= 0;
         int all, rank = scan_exclusive(count, &all, shared) + have;
         have += all;
 #pragma unroll
@@ -197,7 +197,7 @@ __global__ __launch_bounds__(kScan) void kv_fork_plan_kernel(PoolArgs a)
             const int p = p0 + kCells * tid + j;
             if (p >= a.pages)
                 break;
-            const bool free = r[j] == 0;
+            const bool free = r[j] <= 0;
             if (a.refs_out != a.refs)
                 a.refs_out[p] = r[j];
             if (free && rank < need)

@@ -50,3 +50,25 @@ def test_a_child_of_a_partial_page_that_does_not_exist_reads_zeros(hkv, page, d,
         assert torch.equal(_rows(after[p], t[1].tolist(), n), _rows(cache[p], tables[0], n)), f"plane {p}"
     others = [p for p in range(pages) if p != 3]
     assert torch.equal(after[:, others], cache[:, others]) and torch.equal(after[:, 3, :, rest:], cache[:, 3, :, rest:])
+
+
+def test_a_page_released_too_often_is_free_to_both_calls():
+    """A count below zero: compacting drops the page, so forking may take it."""
+    _, q_ = gpu_or_skip()
+    print("negative references", flush=True)
+    cache = torch.arange(6 * 16 * 8, dtype=torch.int16).view(1, 6, 1, 16, 8)
+    start = [[1, -1, 0, 1, -7, 1], [[0, 3, -1], [-1, -1, -1], [5, -1, -1]], [20, 0, 16]]
+    dev, r, t, lens = cache.to(DEV).view(torch.float16), *(_ints(x) for x in start)
+    status = q_.tf_kv_fork(dev, r, t, lens, _ints([0]), _ints([1]))
+    torch.cuda.synchronize()
+    assert status.tolist() == [0] and r.tolist() == [2, 1, 0, 1, -7, 1] and t[1].tolist() == [0, 1, -1]
+    assert torch.equal(dev[0, 1, :, :4].cpu().view(torch.int16), cache[0, 3, :, :4])
+    moved = q_.tf_kv_compact(dev, r, t)
+    torch.cuda.synchronize()
+    assert moved.tolist() == [0, 1, -1, 3, -1, 2] and r.tolist() == [2, 1, 1, 1, 0, 0]
+    assert t.tolist() == [[0, 3, -1], [0, 1, -1], [2, -1, -1]]
+    # short of pages by one: the zero and the negative page both count
+    r, t, lens = (_ints(x) for x in ([1, -1, 0, 1], [[0, 3], [-1, -1], [-1, -1], [-1, -1]], [20, 0, 0, 0]))
+    status = q_.tf_kv_fork(dev[:, :4].contiguous(), r, t, lens, _ints([0, 0, 0]), _ints([1, 2, 3]))
+    torch.cuda.synchronize()
+    assert status.tolist() == [1]

@@ -3,8 +3,9 @@ module that marshals the attention and cache calls (_calls.so).
 
 Every HIP source is compiled with hipcc for gfx950 only; packed-fp32 code
 generation is switched off for all device code.  _calls.so is plain C++ against
-torch's headers.  The results land next to this file, where the binding loads
-them.
+torch's headers, by the same compiler; where torch is not installed, so that the
+library serves C programs alone, it is left out.  The results land next to this
+file, where the binding loads them.
 """
 
 from __future__ import annotations
@@ -39,18 +40,21 @@ def compile_flags() -> list[str]:
             "-I", INCLUDE, "-I", CSRC]
 
 
-def _compile_calls() -> str:
-    import torch
+def _compile_calls() -> str | None:
+    try:
+        import torch
+    except ModuleNotFoundError:
+        return None
     from torch.utils.cpp_extension import include_paths
 
     obj = os.path.join(BUILD_DIR, "torch_calls.o")
     abi = int(torch._C._GLIBCXX_USE_CXX11_ABI)
     includes = [x for path in (*include_paths(), sysconfig.get_paths()["include"]) for x in ("-isystem", path)]
-    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-Wall", f"-D_GLIBCXX_USE_CXX11_ABI={abi}", "-I", INCLUDE, *includes,
-           "-c", os.path.join(CSRC, "torch_calls.cpp"), "-o", obj]
+    cmd = [hipcc(), "-x", "c++", "-O2", "-std=c++17", "-fPIC", "-Wall", f"-D_GLIBCXX_USE_CXX11_ABI={abi}", "-I", INCLUDE,
+           *includes, "-c", os.path.join(CSRC, "torch_calls.cpp"), "-o", obj]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode:
-        raise RuntimeError(f"g++ failed on torch_calls.cpp:\n{r.stdout}{r.stderr}")
+        raise RuntimeError(f"hipcc failed on torch_calls.cpp:\n{r.stdout}{r.stderr}")
     return obj
 
 
@@ -58,7 +62,7 @@ def _link_calls(obj: str) -> None:
     from torch.utils.cpp_extension import library_paths
 
     tmp = CALLS_PATH + f".tmp{os.getpid()}"
-    cmd = ["g++", "-shared", "-fPIC", obj, "-o", tmp, "-L", HERE, "-l:libtilefuse.so",
+    cmd = [hipcc(), "-no-hip-rt", "-shared", "-fPIC", obj, "-o", tmp, "-L", HERE, "-l:libtilefuse.so",
            *[f"-L{path}" for path in library_paths()], "-ltorch_python", "-ltorch_cpu", "-ltorch", "-lc10",
            "-Wl,-rpath,$ORIGIN"]
     r = subprocess.run(cmd, capture_output=True, text=True)
@@ -68,7 +72,7 @@ def _link_calls(obj: str) -> None:
 
 
 def build(verbose: bool = False) -> str:
-    """Compile every source and link libtilefuse.so and _calls.so; returns the library's path."""
+    """Compile every source, link libtilefuse.so and, where torch is, _calls.so; returns the library's path."""
     os.makedirs(BUILD_DIR, exist_ok=True)
 
     def one(src):
@@ -92,7 +96,8 @@ def build(verbose: bool = False) -> str:
     if r.returncode:
         raise RuntimeError(f"link failed:\n{r.stdout}{r.stderr}")
     os.replace(tmp, LIB_PATH)
-    _link_calls(calls.result())
+    if calls.result():
+        _link_calls(calls.result())
     return LIB_PATH
 
 

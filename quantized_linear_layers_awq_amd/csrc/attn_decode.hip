@@ -223,8 +223,8 @@ template <int D, bool F16, int NT, int W, bool SHARES> __global__ __launch_bound
             }
             float top = fmaxf(fmaxf(fmaxf(x[0][0], x[0][1]), fmaxf(x[0][2], x[0][3])),
                               fmaxf(fmaxf(x[1][0], x[1][1]), fmaxf(x[1][2], x[1][3])));
-            top = max_swap32(max_swap16(top)) * a.scale_log2 - kHeadroom<F16>;
-            if (__builtin_amdgcn_ballot_w64(top > m[nt] + kRescaleSlack)) {
+            top = held_maximum<F16>(max_swap32(max_swap16(top)) * a.scale_log2);
+            if (__builtin_amdgcn_ballot_w64(top - m[nt] > kRescaleSlack)) {
                 const float to = fmaxf(m[nt], top), f = exp2_fast(m[nt] - to);
                 m[nt] = to;
                 l[nt] *= f;
@@ -232,13 +232,18 @@ template <int D, bool F16, int NT, int W, bool SHARES> __global__ __launch_bound
                 for (int t = 0; t < kTiles; ++t)
                     o[nt][t] *= f;
             }
+            float by = a.scale_log2;
+            if (__builtin_amdgcn_ballot_w64(fabsf(m[nt]) >= kLargeScore)) { // rare
+                x[0] *= by, x[1] *= by;
+                by = 1.f;
+            }
             // P rounds to the inputs' type for the MFMA; the sum is taken over the
             // rounded values (a product with ones), so that rounding cancels
             // where a row's weight sits on few keys
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-                p[nt][j] = pack_half_x2<F16>(exp2_fast(x[j >> 1][2 * (j & 1)] * a.scale_log2 - m[nt]),
-                                             exp2_fast(x[j >> 1][2 * (j & 1) + 1] * a.scale_log2 - m[nt]));
+                p[nt][j] = pack_half_x2<F16>(exp2_fast(x[j >> 1][2 * (j & 1)] * by - m[nt]),
+                                             exp2_fast(x[j >> 1][2 * (j & 1) + 1] * by - m[nt]));
             l[nt] = mfma16x16x32<F16>(ones, p[nt], l[nt]);
         }
 #pragma unroll

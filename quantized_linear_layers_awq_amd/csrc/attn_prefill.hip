@@ -269,16 +269,22 @@ template <int D, bool F16, bool PAGED> __global__ __launch_bounds__(64 * kWaves,
             t1 = fmaxf(fmaxf(t1, y[1][i]), y[1][i + 1]);
         }
         t0 = fmaxf(fmaxf(t0, y[0][15]), t1);
-        return max_swap32(fmaxf(t0, y[1][15])) * a.scale_log2 - kHeadroom<F16>;
+        return held_maximum<F16>(max_swap32(fmaxf(t0, y[1][15])) * a.scale_log2);
     };
+    float by; // what the scores x are still to be multiplied with
     auto raise = [&](float top) {
-        if (__builtin_amdgcn_ballot_w64(top > m + kRescaleSlack)) {
+        if (__builtin_amdgcn_ballot_w64(top - m > kRescaleSlack)) {
             const float to = fmaxf(m, top), f = exp2_fast(m - to);
             m = to;
             l *= f;
 #pragma unroll
             for (int c = 0; c < kTiles; ++c)
                 o[c] *= f;
+        }
+        by = a.scale_log2;
+        if (__builtin_amdgcn_ballot_w64(fabsf(m) >= kLargeScore)) { // rare
+            x[0] *= by, x[1] *= by;
+            by = 1.f;
         }
     };
     // An infinity or NaN in V at a key that some rows do not see: 0 V would
@@ -331,8 +337,8 @@ template <int D, bool F16, bool PAGED> __global__ __launch_bounds__(64 * kWaves,
             scores(t + 1, y);
 #pragma unroll
         for (int i = 0; i < 32; i += 2) {
-            const uint32_t w = pack_half_x2<F16>(exp2_fast(x[i >> 4][i & 15] * a.scale_log2 - m),
-                                                 exp2_fast(x[i >> 4][(i & 15) + 1] * a.scale_log2 - m));
+            const uint32_t w = pack_half_x2<F16>(exp2_fast(x[i >> 4][i & 15] * by - m),
+                                                 exp2_fast(x[i >> 4][(i & 15) + 1] * by - m));
             p[i >> 3][(i & 7) >> 1] = w;
             l = dot_ones<F16>(w, l);
         }
@@ -352,8 +358,8 @@ template <int D, bool F16, bool PAGED> __global__ __launch_bounds__(64 * kWaves,
                 o[c] = mfma32x32x16<F16>(u32x4{lo[0], lo[1], hi[0], hi[1]}, p[ks], o[c]);
             }
         if constexpr (more) {
-            raise(top);
             x[0] = y[0], x[1] = y[1];
+            raise(top);
         }
     };
 

@@ -29,6 +29,16 @@ constexpr float kRescaleSlack = 8.0f;
 // numbers are 2^-24, and a long row's many small weights must not round to
 // zero there.  p reaches 2^15 at most, inside fp16; bf16 has fp32's range.
 template <bool F16> constexpr float kHeadroom = F16 ? 7.0f : 0.0f;
+// s c - m is one fused operation, m a rounded product: they differ by half a
+// step of m, 2^-4 below this size.  Scores past it, whose steps reach whole
+// powers of two (2^32: 2^8), are multiplied first, rounded as m was, so that
+// the largest one's weight is not 2^(half a step), infinite or zero.  Their m
+// is held at the maximum itself, for there steps swallow the headroom.
+constexpr float kLargeScore = 1048576.0f;
+template <bool F16> __device__ __forceinline__ float held_maximum(float top)
+{
+    return F16 ? top - (fabsf(top) < kLargeScore ? kHeadroom<F16> : 0.f) : top;
+}
 
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
 

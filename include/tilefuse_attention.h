@@ -74,10 +74,10 @@ int tf_kv_append(int type, const uint16_t *qkv, int64_t qkv_token, const float *
 /* Attention.  Scores are scale q . k with fp32 sums, the softmax statistics */
 /* and the outputs' sums are fp32, probabilities are rounded to the tensors' */
 /* type (nearest even) before they meet V, outputs are rounded once.  scale  */
-/* is finite and positive (else TF_ERR_UNSUPPORTED).  D is 64 or 128, Hq / Hkv */
-/* at most 1024 (else TF_ERR_UNSUPPORTED).  A row that sees no key is zero.  */
-/* Keys and values that a row does not see do not reach it, whatever they    */
-/* hold, infinities and NaN included.                                        */
+/* is positive and scale * log2(e) finite, D is 64 or 128, Hq / Hkv at most  */
+/* 1024 (else TF_ERR_UNSUPPORTED).  A row that sees no key is zero.  Keys    */
+/* and values that a row does not see do not reach it, whatever they hold,   */
+/* infinities and NaN included.                                              */
 /* ------------------------------------------------------------------------ */
 
 /* One new token per sequence over its pages.

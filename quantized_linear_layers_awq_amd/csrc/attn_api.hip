@@ -67,9 +67,10 @@ int check_strided(const void *p, int64_t token, int64_t head, int64_t heads, int
     return aligned(p, 16) && token % 8 == 0 && (heads == 1 || head % 8 == 0) ? TF_OK : TF_ERR_ALIGN;
 }
 
-bool scale_ok(float s) { return std::isfinite(s) && s > 0.f; }
-
 constexpr float kLog2E = 1.4426950408889634f;
+
+// the kernels multiply with scale log2(e)
+bool scale_ok(float s) { return std::isfinite(s * kLog2E) && s > 0.f; }
 
 // Rows of a decode call's partial results, and its workspace: the rows, their
 // maxima and sums, three numbers per share.

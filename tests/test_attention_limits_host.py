@@ -1,11 +1,11 @@
-"""The largest launches of the attention and cache calls, without a GPU: a launch
-has fewer than 2^32 threads, and a call past that is refused as a shape before
-anything runs.  At the limit the arguments pass every check and end in
-TF_ERR_HIP, for no device is there."""
+"""The largest launches and scales of the attention and cache calls, without a
+GPU: a launch has fewer than 2^32 threads, and a call past that is refused as a
+shape before anything runs.  At the limit the arguments pass every check and end
+in TF_ERR_HIP, for no device is there."""
 
 import pytest
 
-from test_attention_host import HIP, SHAPE, call, needs_no_gpu
+from test_attention_host import HIP, SHAPE, UNSUPPORTED, call, needs_no_gpu
 
 MOST = (2**32 - 1) // 256  # workgroups of 256 threads
 
@@ -41,3 +41,10 @@ def test_fork_workgroups():
     assert call("tf_kv_fork", forks=0, seqs=MOST) == HIP
     assert call("tf_kv_fork", forks=0, seqs=MOST + 1) == SHAPE
     assert call("tf_kv_fork", planes=2**62, forks=2) == SHAPE
+
+
+@needs_no_gpu
+@pytest.mark.parametrize("name", ["tf_attn_decode", "tf_attn_prefill", "tf_attn_prefill_paged"])
+def test_scale_times_log2_e_is_finite(name):
+    assert call(name, scale=2.3e38) == HIP and call(name, scale=1e-45) == HIP
+    assert call(name, scale=2.4e38) == UNSUPPORTED and call(name, scale=3.4e38) == UNSUPPORTED

@@ -18,7 +18,6 @@
 // them.
 #include <Python.h>
 
-#include <algorithm>
 #include <cmath>
 #include <string>
 
@@ -151,7 +150,7 @@ struct Strides {
         if (t.stride(2) != 1 && t.numel() && t.size(2) > 1)
             refuse(c.fn, std::string("the channels of ") + name + " must be contiguous " + text_of(t));
         head = t.size(1) > 1 ? t.stride(1) : t.size(2);
-        token = t.size(0) > 1 ? t.stride(0) : std::max(t.stride(0), t.size(1) * t.size(2));
+        token = t.size(0) > 1 ? t.stride(0) : t.size(1) * t.size(2);
     }
 };
 

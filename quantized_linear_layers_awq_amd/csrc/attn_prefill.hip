@@ -379,9 +379,11 @@ template <int D, bool F16, bool PAGED> __global__ __launch_bounds__(64 * kWaves,
         raise(highest(x));
         // Before tile t: its values and the next tile's keys are there for
         // everybody, and the buffers of the values before and of its own keys
-        // are used up.
+        // are used up: every wave's reads of them have returned (their products
+        // need not have run).
         auto turn = [&](int t, auto check) {
             wait_vmcnt<0>();
+            wait_lgkmcnt0();
             asm volatile("" ::: "memory"); // no read of LDS moves above the wait
             if constexpr (check) {
                 uint32_t w = 0;

@@ -309,7 +309,6 @@ template <int D, bool F16, bool PAGED> __global__ __launch_bounds__(64 * kWaves,
                         }
                     }
                 }
-        wait_lgkmcnt0();
         lds_barrier();
 #pragma unroll 1
         for (int i = 0; i < kDmas; ++i) { // this wave's rows
@@ -322,7 +321,6 @@ template <int D, bool F16, bool PAGED> __global__ __launch_bounds__(64 * kWaves,
             }
             *p = v;
         }
-        wait_lgkmcnt0();
         lds_barrier();
     };
 
@@ -383,7 +381,6 @@ template <int D, bool F16, bool PAGED> __global__ __launch_bounds__(64 * kWaves,
         // need not have run).
         auto turn = [&](int t, auto check) {
             wait_vmcnt<0>();
-            wait_lgkmcnt0();
             asm volatile("" ::: "memory"); // no read of LDS moves above the wait
             if constexpr (check) {
                 uint32_t w = 0;
@@ -396,7 +393,6 @@ template <int D, bool F16, bool PAGED> __global__ __launch_bounds__(64 * kWaves,
                 const bool any = __builtin_amdgcn_ballot_w64(w != 0) != 0;
                 if (lane == 0)
                     s_bad[t & 1][wave] = any;
-                wait_lgkmcnt0();
             }
             lds_barrier();
             if (t + 1 < tiles)

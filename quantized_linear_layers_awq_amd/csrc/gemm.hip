@@ -452,7 +452,6 @@ __global__ __launch_bounds__(kGThreads, 1) void gemm_kernel(const uint16_t *__re
     start_chain(ic<0>{}, 0, 0);
     if constexpr (kMode != kGWhole)
         start_chain(ic<1>{}, 1, one_tile ? 1 : 0);
-    wait_lgkmcnt0();
     lds_barrier();
 
     // ---- one k-tile (two stages of four slices).  PAR is the chain of
@@ -566,7 +565,6 @@ __global__ __launch_bounds__(kGThreads, 1) void gemm_kernel(const uint16_t *__re
                 wait_vmcnt<kAJ + 2>();
             else
                 wait_vmcnt<kAJ + 1>();
-            wait_lgkmcnt0();
             lds_barrier();
         });
     };

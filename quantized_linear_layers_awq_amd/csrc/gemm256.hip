@@ -402,7 +402,6 @@ __global__ __launch_bounds__(kThreads, 1) void gemm256_kernel(const uint16_t *__
             }
         });
         wait_vmcnt<0>();
-        wait_lgkmcnt0();
         lds_barrier();
     };
     // Row tiles of the wave below M: a last row tile with fewer than 256

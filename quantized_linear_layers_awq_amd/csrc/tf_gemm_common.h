@@ -31,12 +31,14 @@ template <int N> __device__ __forceinline__ void wait_vmcnt()
 }
 __device__ __forceinline__ void wait_lgkmcnt0() { __builtin_amdgcn_s_waitcnt(15 | (3 << 14) | (7 << 4)); }
 
-// Workgroup barrier for LDS filled by LDS-DMA: each wave has already waited
-// for its own loads; the empty asm statements keep the compiler from moving
-// memory operations across the barrier.
+// Workgroup barrier for LDS, also where LDS-DMA fills it (each wave has then
+// already waited for its own copies): this wave's reads and writes of LDS have
+// completed before it; the empty asm statements keep the compiler from moving
+// memory operations across the wait and the barrier.
 __device__ __forceinline__ void lds_barrier()
 {
     asm volatile("" ::: "memory");
+    wait_lgkmcnt0();
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
 }

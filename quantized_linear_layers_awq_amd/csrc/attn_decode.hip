@@ -28,8 +28,8 @@
 //    us, and 59 without).
 // Measured, with the reading rate of a plain stream at 7.0 TB/s: 16 contexts of
 // up to 32768 tokens, 8 heads of 128 channels, 171 us (6.6 TB/s); one of 131072
-// 88 us (6.1: the kernel alone runs at 6.5, the join takes 5 us); 48 ragged ones
-// of up to 4096, 4 heads, 47 us (5.1); one of 333 tokens 6.3 us, which is the
+// 87 us (6.2: the kernel alone runs at 6.6, the join takes 5 us); 48 ragged ones
+// of up to 4096, 4 heads, 45 us (5.3); one of 333 tokens 6.5 us, which is the
 // latency of the chain length, pages, keys, join.
 #include "tf_attn.h"
 
@@ -237,9 +237,11 @@ template <int D, bool F16, int NT, int W, bool SHARES> __global__ __launch_bound
                 x[0] *= by, x[1] *= by;
                 by = 1.f;
             }
-            // P rounds to the inputs' type for the MFMA; the sum is taken over the
-            // rounded values (a product with ones), so that rounding cancels
-            // where a row's weight sits on few keys
+            // P rounds to the inputs' type, the operands' of the MFMA (error
+            // against 64 bits 1.6e-3 in the plain fp32 form and 1.7e-3 here,
+            // bf16, the output's rounding the most of both); the sum is taken
+            // over the rounded values (a product with ones), so that rounding
+            // cancels where a row's weight sits on few keys
 #pragma unroll
             for (int j = 0; j < 4; ++j)
                 p[nt][j] = pack_half_x2<F16>(exp2_fast(x[j >> 1][2 * (j & 1)] * by - m[nt]),
@@ -493,8 +495,12 @@ template <int D, bool F16> hipError_t run_d(const DecodeArgs &a, const DecodePla
 } // namespace
 
 // Query heads of a key-value head are covered by groups of nt tiles of 16, at
-// most three (the accumulators of more do not fit the registers beside two
-// stages).
+// most three, each of which reads the cache.  The registers of one tile and, of
+// 64 channels, of all three (215) hold two stages; of 128, two tiles have one
+// stage (244), and three, with one stage, spill 56 or 57 registers in shares.
+// 32768 tokens at most: 32 contexts of 48/1 heads of 128 95 us (3.0 TB/s), 16 of
+// 40/2 59 (4.8); of 64, 64 contexts of 48/1 66 (4.6), and of 71/1, two groups
+// that fetch it twice, 110 (2.7).
 // Equal shares cost a look for the share's start and the join.  A workgroup per
 // item is quicker where an item is two tiles a wave at most (one sequence, 8
 // heads: 7.7 us for 512 tokens, and 8.8 for 513 in shares; past that each tile a

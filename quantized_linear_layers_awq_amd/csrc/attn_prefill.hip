@@ -14,10 +14,11 @@
 //    heads, token-major, so heads that share keys share tiles of them for any
 //    G, and a tile of rows spans few tokens (little waste at the diagonal).
 //    A workgroup of 4 waves takes 128 rows, 32 per wave, one row per MFMA
-//    column (32x32x16); two workgroups run on a compute unit.  (64 rows a
-//    wave, one wave a SIMD, halves the reads of LDS but left nothing to run
-//    in a wave's waits: 8192 tokens 655 us, and 512 so; 8 waves sharing the
-//    tiles of 256 rows: 503 for those, but a third more where rows are few.)
+//    column (32x32x16); two workgroups run on a compute unit, three for heads
+//    of 64 channels (166 to 168 registers).  (64 rows a wave, one wave a SIMD,
+//    halves the reads of LDS but left nothing to run in a wave's waits: 8192
+//    tokens 655 us, and 512 so; 8 waves sharing the tiles of 256 rows: 503 for
+//    those, but a third more where rows are few.)
 //  - K and V come in tiles of 64 keys by LDS-DMA, two buffers each, the next
 //    tile's copies running while this one is computed: one barrier per tile.
 //    Units of 16 bytes are XOR-swizzled by row on the way in, K so that 16
@@ -35,12 +36,16 @@
 //    does not have (7 prompts of up to 1553, 32/8 heads: 120 us, and 142 with
 //    those).
 //  - Few rows behind many keys: the keys are cut into ranges and joined.
-// Measured: one prompt of 8192 tokens, 32/8 heads of 128, 494 to 525 us by the
-// board (1050 to 1110 TFLOP/s; a library product of 8192 x 8192 matrices runs at 1116, of
-// 16384 at 1348), MFMAs busy 55 % of 1.87 GHz.  Without the exponentials, the
-// maximum and the sum the same loop takes 480: the matrix units and the power
-// they draw bound it.  For 64 channels, with as many exponentials for half the
-// products, the vector unit does: 71/1 heads, 3 prompts of up to 2048, 690.
+// Measured: one prompt of 8192 tokens, 32/8 heads of 128, 510 to 520 us by the
+// board (1055 to 1080 TFLOP/s; a library product of 8192 x 8192 matrices runs at 1116, of
+// 16384 at 1348) at 1.81 to 1.87 GHz, where the power limit holds the clock.  MFMAs
+// are busy 56 % of its cycles, the vector unit issues in 45 %: together 101 %, they
+// seldom run beside each other.  With 64 channels, as many exponentials for
+// half the products, 298 us (923 TFLOP/s): MFMAs 46 %, vector issue 66 %.
+// Neither is full alone, and the waves spend 42 and 46 % of their time waiting
+// to issue.  A copy of the loop without maximum, exponentials and sum takes 457
+// and 228 (1205 TFLOP/s both).  71/1 heads of 64, 3 prompts of up to 2048: 107
+// us (735).
 #include "tf_attn.h"
 
 namespace tf {
@@ -51,7 +56,7 @@ constexpr int kWaves = 4;
 constexpr int kKeys = 64;
 constexpr int kMinRange = 4;   // tiles of a range of keys, at least
 constexpr int kMaxSplits = 16; // ranges
-constexpr int64_t kSlots = 512; // workgroups that run at a time
+constexpr int64_t kSlots = 512; // workgroups that run at a time, two a compute unit (of 64 channels 768 would)
 constexpr int64_t kL2Share = 3 << 20; // bytes of an XCD's 4 MiB for the keys and values in use
 
 // tiles of a range when the keys of a sequence are cut into `splits`
@@ -325,9 +330,13 @@ template <int D, bool F16, bool PAGED> __global__ __launch_bounds__(64 * kWaves,
     };
 
     // Tile t: p from its scores x, while the products of the next tile's
-    // scores run; then P V, while the next scores' maximum is taken.  The sum
-    // is taken over the rounded p, so that their rounding cancels where a
-    // row's weight sits on few keys.
+    // scores run; then P V, while the next scores' maximum is taken.  p rounds
+    // to the inputs' type, for MFMA operands of 16 bits are what V is read in;
+    // a second product with what the rounding leaves would double P V.  It
+    // moves the error against 64 bits from 1.7e-3 of the plain fp32 form to at
+    // most 1.8e-3 (bf16; the output's own rounding is the most of both).  The sum
+    // is taken over the rounded p, so that their rounding cancels where a row's
+    // weight sits on few keys.
     auto step = [&](int t, auto more, auto masked) {
         f32x16 y[2];
         u32x4 p[4];
@@ -507,11 +516,12 @@ template <int D, bool F16, bool PAGED> hipError_t run(const PrefillArgs &a, int6
 
 // Few row blocks: the keys of a sequence are cut into ranges, so that the
 // device is filled (two workgroups a compute unit), and joined.  A workgroup
-// takes some 4 us and 1.2 us a tile, the join 4 to 8 us, so it pays only where
-// there are several ranges to a block and a range has some tiles: 409 new
-// tokens behind 7783, 8 heads on one, 121 blocks: 148 us whole, 91 in two
-// ranges, 78 in four; but 1000 tokens, 32/8 heads, 250 blocks: 23 us whole, 34
-// in two, and 500 tokens, 128 blocks: 15 us whole, 19 in two.
+// takes some 5 us and 1.2 us a tile alone on a compute unit (2 beside another),
+// the join 4 to 8 us, so it pays only where there are several ranges to a block
+// and a range has some tiles: 1931 new tokens behind 6261, 8 heads on one, 121
+// blocks: 148 us whole, 91 in two ranges, 78 in four; but 1000 tokens, 32/8
+// heads, 256 blocks: 23 us whole, 34 in two, and 500 tokens, 128 blocks: 15 us
+// whole, 19 in two.
 int plan_prefill_splits(int64_t seqs, int64_t T, int64_t hkv, int64_t G, int64_t longest, int64_t keys, int cus)
 {
     const int64_t blocks = hkv * std::min(seqs * prefill_blocks(longest, G), T * G / kPrefillRows + seqs);

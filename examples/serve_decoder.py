@@ -62,7 +62,9 @@ class Cache:
         seq, pos = [], []
         for s, n in more.items():
             for c in range(-(-lens[s] // self.page), -(-(lens[s] + n) // self.page)):
-                tables[s][c] = next(free)
+                tables[s][c] = next(free, None)
+                if tables[s][c] is None:
+                    raise RuntimeError("no page is free")
                 refs[tables[s][c]] = 1
             seq += [s] * n
             pos += range(lens[s], lens[s] + n)

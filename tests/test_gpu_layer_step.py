@@ -90,3 +90,21 @@ def test_append_then_attention_from_the_qkv_output_on(t):
         for s, n in enumerate(now):
             qd, kd, vd = exact(s)
             assert _error(out[s:s + 1], qd[n - 1:n], kd[:n], vd[:n], torch.tensor([n], device=DEV), scale, hkv, t) <= 1.0
+
+
+def test_the_example_says_when_no_page_is_free():
+    import importlib.util
+    import os
+
+    from conftest import ROOT
+
+    gpu_or_skip()
+    spec = importlib.util.spec_from_file_location("serve_decoder", os.path.join(ROOT, "examples", "serve_decoder.py"))
+    example = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(example)
+    cache = example.Cache(layers=1, pages=2, hkv=1, page=16, d=64, seqs=2, width=4)
+    cache.reserve({0: 20})
+    with pytest.raises(RuntimeError, match="no page is free"):
+        cache.reserve({1: 1})
+    # what was there before is as it was
+    assert cache.lens.tolist() == [20, 0] and cache.refs.tolist() == [1, 1] and cache.tables[1].tolist() == [-1] * 4

@@ -123,8 +123,8 @@ int tf_attn_prefill(int type, const uint16_t *q, int64_t q_token, int64_t q_head
 /* The same over the pages of a cache that already holds the sequences' lens[s]
  * tokens, the new ones included (prompts in chunks, shared prefixes).  `keys`
  * of the workspace's size is width * page, and the work is ordered and split for
- * that many: tables far wider than the lengths are answered alike but later than
- * tables cut to them. */
+ * that many: a single short prompt over a table for 131072 tokens takes 2 to 4 us
+ * longer than over one cut to its length. */
 int tf_attn_prefill_paged(int type, const uint16_t *q, int64_t q_token, int64_t q_head, const uint16_t *k_pages,
                           const uint16_t *v_pages, int64_t pages, int64_t page, const int32_t *tables, int64_t width,
                           const int32_t *cu_q, const int32_t *lens, uint16_t *out, int64_t seqs, int64_t T, int64_t Hq,
